@@ -863,4 +863,150 @@ sala_status sala_sparse_decode_paged(const void* q, const void* k_pages, const v
     return launched(e, "sparse_decode_paged");
 }
 
+// ----------------------------------------------------------------------------------------------
+// Dense serving path
+
+static sala_status check_dense(int B, int Hkv, int d, sala_dtype dt) {
+    REQUIRE(B >= 0, SALA_ERR_INVALID_ARG, "negative batch %d", B);
+    REQUIRE(Hkv > 0, SALA_ERR_INVALID_ARG, "Hkv %d must be positive", Hkv);
+    REQUIRE(dt == SALA_F32 || dt == SALA_BF16, SALA_ERR_INVALID_ARG, "unknown dtype %d", (int)dt);
+    REQUIRE(d == 64 || d == 128, SALA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", d);
+    return SALA_OK;
+}
+
+static sala_status check_heads(int H, int Hkv, float scale) {
+    REQUIRE(H >= 0 && H % Hkv == 0, SALA_ERR_INVALID_ARG, "H %d must be a multiple of Hkv %d", H, Hkv);
+    REQUIRE(isfinite(scale) && scale >= 0.f, SALA_ERR_INVALID_ARG, "scale must be finite and >= 0");
+    return SALA_OK;
+}
+
+// The page pool: sizes, format and pointers.
+static sala_status check_pages(const void* k_pages, const void* v_pages, const float* k_scale,
+                               const float* v_scale, int n_pages, const int32_t* page_table,
+                               int max_pages, int Hkv, int block, sala_kv_format fmt) {
+    REQUIRE(block == 64, SALA_ERR_UNSUPPORTED, "block %d (pages hold 64 tokens)", block);
+    REQUIRE(n_pages >= 0 && max_pages >= 0, SALA_ERR_INVALID_ARG, "negative page counts");
+    REQUIRE((int64_t)n_pages * Hkv * 64 <= 0x7fffffffll, SALA_ERR_UNSUPPORTED,
+            "a pool of more than 2^31 - 1 rows (%d pages, %d KV heads)", n_pages, Hkv);
+    REQUIRE(fmt == SALA_KV_SAME || fmt == SALA_KV_INT8 || fmt == SALA_KV_E4M3, SALA_ERR_INVALID_ARG,
+            "unknown cache format %d", (int)fmt);
+    REQ_PTR(k_pages); REQ_PTR(v_pages);
+    REQUIRE(page_table != nullptr, SALA_ERR_INVALID_ARG, "page_table must be a device pointer");
+    if (fmt == SALA_KV_SAME) {
+        REQUIRE(k_scale == nullptr && v_scale == nullptr, SALA_ERR_INVALID_ARG,
+                "k_scale and v_scale belong to the 8-bit cache formats");
+    } else {
+        REQ_PTR(k_scale); REQ_PTR(v_scale);
+    }
+    return SALA_OK;
+}
+
+sala_status sala_packed_prefill(const void* q, const void* k, const void* v,
+                                const int32_t* cu_seqlens, void* o, int B, int H, int Hkv,
+                                int total, int d, float scale, sala_dtype dt, sala_stream stream) {
+    sala_status s = check_dense(B, Hkv, d, dt);
+    if (s != SALA_OK) return s;
+    if ((s = check_heads(H, Hkv, scale)) != SALA_OK) return s;
+    REQUIRE(total >= 0, SALA_ERR_INVALID_ARG, "negative size (total=%d)", total);
+    if (B == 0 || H == 0 || total == 0) return SALA_OK;
+    REQ_PTR(q); REQ_PTR(k); REQ_PTR(v); REQ_PTR(o);
+    REQUIRE(cu_seqlens != nullptr, SALA_ERR_INVALID_ARG, "cu_seqlens must be a device pointer");
+    if (scale == 0.f) scale = 1.0f / sqrtf((float)d);
+    sala::DevCtx ctx;
+    if ((s = get_ctx(&ctx)) != SALA_OK) return s;
+    const cudaError_t e = sala::launch_packed_simt(to_dt(dt), q, k, v, cu_seqlens, o, B, H, Hkv,
+                                                   total, d, scale, static_cast<cudaStream_t>(stream), ctx);
+    if (e == cudaErrorNotSupported) return fail(SALA_ERR_UNSUPPORTED, "more than 65535 query heads");
+    return launched(e, "packed_prefill");
+}
+
+sala_status sala_kv_write(const void* k, const void* v, const int32_t* cu_seqlens,
+                          const int32_t* pos, const int32_t* page_table, int max_pages,
+                          void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                          int n_pages, int B, int Hkv, int total, int d, int block,
+                          sala_kv_format fmt, sala_dtype dt, sala_stream stream) {
+    sala_status s = check_dense(B, Hkv, d, dt);
+    if (s != SALA_OK) return s;
+    REQUIRE(total >= 0, SALA_ERR_INVALID_ARG, "negative size (total=%d)", total);
+    if (B == 0 || total == 0) return SALA_OK;
+    if ((s = check_pages(k_pages, v_pages, k_scale, v_scale, n_pages, page_table, max_pages, Hkv,
+                         block, fmt)) != SALA_OK)
+        return s;
+    REQ_PTR(k); REQ_PTR(v);
+    REQUIRE(cu_seqlens != nullptr && pos != nullptr, SALA_ERR_INVALID_ARG,
+            "cu_seqlens and pos must be device pointers");
+    sala::DevCtx ctx;
+    if ((s = get_ctx(&ctx)) != SALA_OK) return s;
+    const sala::KvPages p{k_pages, v_pages, k_scale, v_scale, page_table, max_pages, n_pages};
+    return launched(sala::launch_kv_write(to_dt(dt), (sala::KvFormat)fmt, k, v, cu_seqlens, pos, p, B,
+                                          Hkv, total, d, static_cast<cudaStream_t>(stream), ctx),
+                    "kv_write");
+}
+
+sala_status sala_kv_read(const void* k_pages, const void* v_pages, const float* k_scale,
+                         const float* v_scale, int n_pages, const int32_t* page_table,
+                         int max_pages, const int32_t* cu_seqlens, const int32_t* pos, void* k,
+                         void* v, int B, int Hkv, int total, int d, int block, sala_kv_format fmt,
+                         sala_dtype dt, sala_stream stream) {
+    sala_status s = check_dense(B, Hkv, d, dt);
+    if (s != SALA_OK) return s;
+    REQUIRE(total >= 0, SALA_ERR_INVALID_ARG, "negative size (total=%d)", total);
+    if (B == 0 || total == 0) return SALA_OK;
+    if ((s = check_pages(k_pages, v_pages, k_scale, v_scale, n_pages, page_table, max_pages, Hkv,
+                         block, fmt)) != SALA_OK)
+        return s;
+    REQ_PTR(k); REQ_PTR(v);
+    REQUIRE(cu_seqlens != nullptr && pos != nullptr, SALA_ERR_INVALID_ARG,
+            "cu_seqlens and pos must be device pointers");
+    sala::DevCtx ctx;
+    if ((s = get_ctx(&ctx)) != SALA_OK) return s;
+    const sala::KvPages p{k_pages, v_pages, k_scale, v_scale, page_table, max_pages, n_pages};
+    return launched(sala::launch_kv_read(to_dt(dt), (sala::KvFormat)fmt, p, cu_seqlens, pos, k, v, B,
+                                         Hkv, total, d, static_cast<cudaStream_t>(stream), ctx),
+                    "kv_read");
+}
+
+size_t sala_tree_decode_paged_workspace(int B, int H, int Hkv, int T, int max_ctx, int d) {
+    if (B <= 0 || H <= 0 || Hkv <= 0 || T <= 0 || max_ctx < 0 || (d != 64 && d != 128)) return 0;
+    return (sala::tree_simt_workspace(d) + 255) & ~(size_t)255;
+}
+
+sala_status sala_tree_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                                   const float* k_scale, const float* v_scale, int n_pages,
+                                   const int32_t* page_table, int max_pages, const int32_t* ctx_len,
+                                   int max_ctx, const uint64_t* tree, void* o, int B, int H,
+                                   int Hkv, int T, int d, int block, float scale, void* workspace,
+                                   size_t workspace_bytes, sala_kv_format fmt, sala_dtype dt,
+                                   sala_stream stream) {
+    sala_status s = check_dense(B, Hkv, d, dt);
+    if (s != SALA_OK) return s;
+    if ((s = check_heads(H, Hkv, scale)) != SALA_OK) return s;
+    REQUIRE(T >= 0, SALA_ERR_INVALID_ARG, "negative size (T=%d)", T);
+    REQUIRE(T <= 64, SALA_ERR_UNSUPPORTED, "T %d (a row's mask has 64 bits)", T);
+    if (B == 0 || H == 0 || T == 0) return SALA_OK;
+    if ((s = check_pages(k_pages, v_pages, k_scale, v_scale, n_pages, page_table, max_pages, Hkv,
+                         block, fmt)) != SALA_OK)
+        return s;
+    REQUIRE(max_ctx >= 0 && (int64_t)max_ctx + T <= (int64_t)max_pages * 64, SALA_ERR_INVALID_ARG,
+            "max_ctx %d + T %d outside the page table (%d pages of 64 tokens)", max_ctx, T, max_pages);
+    REQUIRE((int64_t)B * Hkv <= 65535, SALA_ERR_UNSUPPORTED, "B * Hkv = %lld above 65535",
+            (long long)B * Hkv);
+    REQUIRE((int64_t)(H / Hkv) * T <= 1 << 20, SALA_ERR_UNSUPPORTED, "more than 2^20 rows per KV head");
+    REQ_PTR(q); REQ_PTR(o);
+    REQUIRE(ctx_len != nullptr && tree != nullptr && ((uintptr_t)tree & 7) == 0, SALA_ERR_INVALID_ARG,
+            "ctx and tree must be device pointers (tree 8-byte aligned)");
+    const size_t need = sala_tree_decode_paged_workspace(B, H, Hkv, T, max_ctx, d);
+    REQUIRE(workspace != nullptr && aligned16(workspace) && workspace_bytes >= need,
+            SALA_ERR_INVALID_ARG, "workspace of %zu bytes (16-byte aligned) required, got %zu", need,
+            workspace_bytes);
+    if (scale == 0.f) scale = 1.0f / sqrtf((float)d);
+    sala::DevCtx ctx;
+    if ((s = get_ctx(&ctx)) != SALA_OK) return s;
+    const sala::KvPages p{k_pages, v_pages, k_scale, v_scale, page_table, max_pages, n_pages};
+    return launched(sala::launch_tree_simt(to_dt(dt), (sala::KvFormat)fmt, q, p, tree, o, ctx_len,
+                                           max_ctx, B, H, Hkv, T, d, scale, workspace,
+                                           static_cast<cudaStream_t>(stream), ctx),
+                    "tree_decode_paged");
+}
+
 }  // extern "C"

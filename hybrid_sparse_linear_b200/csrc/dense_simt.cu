@@ -1,0 +1,365 @@
+// Dense softmax attention on the CUDA cores, for packed prompts and for drafted tokens over a
+// paged cache: the fp32 form of both (the bf16 form runs on the tensor cores).
+//
+// One block takes 64 query rows and walks 64-key tiles with the running maximum and sum of the
+// softmax in registers: S = Q K^T as 4 x 4 values per thread, P through shared memory, O += P V
+// with 4 x D/16 sums per thread.  Per tile 2 * 64 * 64 * D multiply-adds against 2 * 64 * D loads:
+// bound by the fp32 FMA units once more than one block runs per SM (84 KB each, two per SM).
+// K and V of a tile take turns in one buffer, which is what lets two blocks share an SM.
+//
+// Masked positions are left out by selection, never by adding a large negative number or by
+// multiplying with zero: a hidden key or value may hold an infinity or a NaN without touching the
+// rows that do not see it.  A row that sees no key gives zeros.
+#include <type_traits>
+
+#include "kernels.h"
+#include "kv_format.cuh"
+#include "ptx.cuh"
+#include "tree_plan.cuh"
+
+namespace sala {
+namespace {
+
+constexpr int kRows = 64;   // query rows per block
+constexpr int kKeys = 64;   // keys per tile: one page of the paged cache
+constexpr int kThreads = 256;
+constexpr int kPad = 4;     // floats: 16-byte rows that start 4 banks apart
+constexpr float kHidden = -1.f;  // P of a position its row does not see (probabilities are >= 0)
+
+template <int D>
+constexpr int smem_floats() { return 2 * kRows * (D + kPad) + kRows * (kKeys + kPad); }
+
+// The state of 64 query rows in 256 threads: thread (ty, tx) = (tid / 16, tid % 16) holds rows
+// 4 ty .. 4 ty + 3 and of each the output columns 64 j + 4 tx .. + 3.
+template <int D>
+struct Rows {
+    float m[4], l[4];        // running maximum (scaled log2 units), running sum
+    float acc[4][D / 16];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
+        }
+    }
+};
+
+// One key tile.  load(r, c) gives 4 consecutive floats of key (value) row r; seen(row, key) says
+// whether the row attends to the tile's key; masked: whether any position may be hidden.
+template <int D, class LoadK, class LoadV, class Seen>
+__device__ __forceinline__ void attend_tile(Rows<D>& st, float* sm, float sl2, bool masked,
+                                            LoadK load_k, LoadV load_v, Seen seen) {
+    constexpr int kLd = D + kPad, kLp = kKeys + kPad;
+    float* Q = sm;
+    float* KV = sm + kRows * kLd;
+    float* P = KV + kKeys * kLd;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+        *reinterpret_cast<float4*>(KV + r * kLd + c) = load_k(r, c);
+    }
+    __syncthreads();
+    float s[4][4] = {};
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(Q + (ty * 4 + i) * kLd + c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(KV + (tx + 16 * j) * kLd + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s[i][j] += a[i].x * b[j].x + a[i].y * b[j].y + a[i].z * b[j].z + a[i].w * b[j].w;
+    }
+    // A NaN logit has to reach its row: fmaxf drops it from the maximum, exp2f passes it on.
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        bool vis[4];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            vis[j] = !masked || seen(ty * 4 + i, tx + 16 * j);
+            s[i][j] *= sl2;
+            if (vis[j]) mx = fmaxf(mx, s[i][j]);
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float m_new = fmaxf(st.m[i], mx);
+        const float alpha = st.m[i] == -INFINITY ? 0.f : exp2f(st.m[i] - m_new);
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float p = vis[j] ? (s[i][j] == -INFINITY ? 0.f : exp2f(s[i][j] - m_new)) : kHidden;
+            if (vis[j]) sum += p;
+            P[(ty * 4 + i) * kLp + tx + 16 * j] = p;
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        st.l[i] = st.l[i] * alpha + sum;
+        st.m[i] = m_new;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) st.acc[i][c] *= alpha;
+    }
+    __syncthreads();  // S is done with K
+    for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+        *reinterpret_cast<float4*>(KV + r * kLd + c) = load_v(r, c);
+    }
+    __syncthreads();
+    auto pv = [&](auto hide) {
+#pragma unroll 2
+        for (int k = 0; k < kKeys; k += 4) {
+            float4 p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(P + (ty * 4 + i) * kLp + k);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j) {
+                    const float4 v = *reinterpret_cast<const float4*>(KV + (k + kk) * kLd + 64 * j + 4 * tx);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                        if (decltype(hide)::value && w == kHidden) continue;
+                        st.acc[i][4 * j] += w * v.x;
+                        st.acc[i][4 * j + 1] += w * v.y;
+                        st.acc[i][4 * j + 2] += w * v.z;
+                        st.acc[i][4 * j + 3] += w * v.w;
+                    }
+                }
+        }
+    };
+    if (masked) pv(std::true_type{});
+    else pv(std::false_type{});
+    __syncthreads();  // the next tile writes KV and P
+}
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+    return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(ptx::pack_bf16x2(x.x, x.y), ptx::pack_bf16x2(x.z, x.w));
+}
+
+// Four values of row `row` of the cache's keys or values.
+template <typename T, KvFormat F>
+__device__ __forceinline__ float4 kv_load4(const void* p, const float* scale, int64_t row, int d, int col) {
+    if constexpr (F == KvFormat::Same) {
+        return load4(static_cast<const T*>(p) + row * d + col);
+    } else {
+        const float4 x = decode4<F>(__ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + row * d + col)));
+        const float s = __ldg(scale + row);
+        return make_float4(x.x * s, x.y * s, x.z * s, x.w * s);
+    }
+}
+
+// ---------------------------------------------------------------- packed prompts
+// Block = (64 consecutive tokens of one sequence, one query head); blockIdx.x counts the tiles of
+// all sequences, an upper bound of which the host launches.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2)
+packed_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                   const int32_t* __restrict__ cu, T* __restrict__ out, int B, int H, int Hkv,
+                   int total, float sl2, DevCtx ctx) {
+    extern __shared__ __align__(16) float sm[];
+    __shared__ PackedTile tile;
+    const int tid = threadIdx.x;
+    if (tid < 32) {
+        const PackedTile t = find_packed_tile(cu, B, total, blockIdx.x, kRows, tid, ctx,
+                                              blockIdx.x == 0 && blockIdx.y == 0);
+        if (tid == 0) tile = t;
+    }
+    __syncthreads();
+    const PackedTile t = tile;
+    if (t.len <= 0) return;
+    const int h = blockIdx.y, kvh = h / (H / Hkv);
+    const int64_t row0 = (int64_t)h * total + t.start + t.first;
+    const T* kb = k + ((int64_t)kvh * total + t.start) * D;
+    const T* vb = v + ((int64_t)kvh * total + t.start) * D;
+    const int n_rows = min(kRows, t.len - t.first);
+    constexpr int kLd = D + kPad;
+    for (int e = tid; e < kRows * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+        *reinterpret_cast<float4*>(sm + r * kLd + c) =
+            r < n_rows ? load4(q + (row0 + r) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    Rows<D> st;
+    st.clear();
+    for (int k0 = 0; k0 <= t.first; k0 += kKeys) {
+        const bool masked = k0 + kKeys > t.first;
+        const int n_keys = min(kKeys, t.len - k0);
+        auto load = [&](const T* base, int r, int c) {
+            return r < n_keys ? load4(base + (int64_t)(k0 + r) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        attend_tile<D>(st, sm, sl2, masked, [&](int r, int c) { return load(kb, r, c); },
+                       [&](int r, int c) { return load(vb, r, c); },
+                       [&](int row, int key) { return k0 + key <= t.first + row; });
+    }
+    const int ty = tid >> 4, tx = tid & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        if (r >= n_rows) continue;
+        const float inv = 1.f / st.l[i];  // every row sees itself
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+            store4(out + (row0 + r) * D + 64 * j + 4 * tx,
+                   make_float4(st.acc[i][4 * j] * inv, st.acc[i][4 * j + 1] * inv,
+                               st.acc[i][4 * j + 2] * inv, st.acc[i][4 * j + 3] * inv));
+    }
+}
+
+// ---------------------------------------------------------------- drafted tokens, paged cache
+template <typename T, int D, KvFormat F>
+__global__ void __launch_bounds__(kThreads, 2)
+tree_simt_kernel(const T* __restrict__ q, KvPages pages, const uint64_t* __restrict__ masks,
+                 T* __restrict__ out, tree::Shape s, tree::Partials part, float sl2, DevCtx ctx) {
+    extern __shared__ __align__(16) float sm[];
+    __shared__ tree::Cursor cur0;
+    __shared__ uint64_t bits[kRows];
+    const int tid = threadIdx.x;
+    if (tid < 32) {
+        bool bad = false;
+        const long long w = tree::total_tiles(s, tid, &bad);
+        const long long x0 = tree::run_start(w, blockIdx.x, gridDim.x);
+        const long long x1 = tree::run_start(w, blockIdx.x + 1, gridDim.x);
+        const tree::Cursor c = tree::find_tile(s, x0, x1 - x0, tid);
+        if (bad && blockIdx.x == 0) flag(ctx, kStatusBounds);
+        if (tid == 0) cur0 = c;
+    }
+    __syncthreads();
+    tree::Cursor c = cur0;
+    constexpr int kLd = D + kPad;
+    const int ty = tid >> 4, tx = tid & 15;
+    for (bool first = true; c.left > 0; tree::next_item(s, c), first = false) {
+        const int r0 = c.rt * kRows, n_rows = min(kRows, s.rows - r0);
+        const int n = tree::run_tiles(c);
+        const int64_t row0 = ((int64_t)c.b * s.Hkv + c.g) * s.rows + r0;
+        __syncthreads();  // the previous item is done with Q and bits
+        for (int e = tid; e < kRows * (D / 4); e += kThreads) {
+            const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+            *reinterpret_cast<float4*>(sm + r * kLd + col) =
+                r < n_rows ? load4(q + (row0 + r) * D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (tid < kRows) bits[tid] = tid < n_rows ? tree::draft_bits(masks, c.b, (r0 + tid) % s.T, s.T) : 0ull;
+        __syncthreads();
+        Rows<D> st;
+        st.clear();
+        for (int t = c.tile; t < c.tile + n; ++t) {
+            const int k0 = t * kKeys;
+            const int page = page_of(pages, c.b, t);
+            if (page < 0) {  // a page the table does not hold: its keys are left out
+                if (tid == 0) flag(ctx, kStatusBounds);
+                continue;
+            }
+            const int n_keys = min(kKeys, c.ctx + s.T - k0);
+            const int64_t base = ((int64_t)page * s.Hkv + c.g) * kKeys;
+            auto load = [&](const void* p, const float* sc, int r, int col) {
+                return r < n_keys ? kv_load4<T, F>(p, sc, base + r, D, col) : make_float4(0.f, 0.f, 0.f, 0.f);
+            };
+            attend_tile<D>(st, sm, sl2, k0 + kKeys > c.ctx,
+                           [&](int r, int col) { return load(pages.k, pages.k_scale, r, col); },
+                           [&](int r, int col) { return load(pages.v, pages.v_scale, r, col); },
+                           [&](int row, int key) {
+                               const int j = k0 + key - c.ctx;  // draft number
+                               return j < 0 || (j < s.T && ((bits[row] >> j) & 1ull));
+                           });
+        }
+        const bool whole = c.tile == 0 && n == c.n_tiles;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRows;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty * 4 + i;
+            if (r >= n_rows) continue;
+            const float inv = !whole ? 1.f : st.m[i] == -INFINITY && st.l[i] == 0.f ? 0.f : 1.f / st.l[i];
+            if (!whole && tx == 0) part.ml[slot + r] = make_float2(st.m[i], st.l[i]);
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const float4 x = make_float4(st.acc[i][4 * j] * inv, st.acc[i][4 * j + 1] * inv,
+                                             st.acc[i][4 * j + 2] * inv, st.acc[i][4 * j + 3] * inv);
+                if (whole) store4(out + (row0 + r) * D + 64 * j + 4 * tx, x);
+                else store4(part.o + (slot + r) * D + 64 * j + 4 * tx, x);
+            }
+        }
+    }
+}
+
+template <typename T, int D>
+cudaError_t packed_simt(const void* q, const void* k, const void* v, const int32_t* cu, void* o,
+                        int B, int H, int Hkv, int total, float scale, cudaStream_t st, DevCtx ctx) {
+    constexpr int bytes = smem_floats<D>() * 4;
+    if (cudaError_t e = ensure_smem<packed_simt_kernel<T, D>>(bytes); e != cudaSuccess) return e;
+    // every sequence has at most one tile that is not full
+    const long long tiles = (long long)total / kRows + (B < total ? B : total);
+    if (H > 65535 || tiles > 0x7fffffffll) return cudaErrorNotSupported;
+    packed_simt_kernel<T, D><<<dim3((unsigned)tiles, H), kThreads, bytes, st>>>(
+        static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), cu,
+        static_cast<T*>(o), B, H, Hkv, total, scale * 1.4426950408889634f, ctx);
+    return cudaGetLastError();
+}
+
+template <typename T, int D, KvFormat F>
+cudaError_t tree_simt(const void* q, const KvPages& pages, const uint64_t* masks, void* o,
+                      const tree::Shape& s, void* ws, float scale, cudaStream_t st, DevCtx ctx) {
+    constexpr int bytes = smem_floats<D>() * 4;
+    if (cudaError_t e = ensure_smem<tree_simt_kernel<T, D, F>>(bytes); e != cudaSuccess) return e;
+    const int n_cta = tree_simt_ctas();
+    const tree::Partials part = tree::partials_at(ws, n_cta, kRows);
+    tree_simt_kernel<T, D, F><<<n_cta, kThreads, bytes, st>>>(
+        static_cast<const T*>(q), pages, masks, static_cast<T*>(o), s, part,
+        scale * 1.4426950408889634f, ctx);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    return launch_tree_join(std::is_same<T, float>::value ? DType::F32 : DType::BF16, part, o, s, kRows,
+                            D, n_cta, st);
+}
+
+}  // namespace
+
+int tree_simt_ctas() { return 2 * device_sm_count(); }
+size_t tree_simt_workspace(int d) { return tree::partial_bytes(tree_simt_ctas(), kRows, d); }
+
+cudaError_t launch_packed_simt(DType dt, const void* q, const void* k, const void* v,
+                               const int32_t* cu, void* o, int B, int H, int Hkv, int total, int d,
+                               float scale, cudaStream_t st, DevCtx ctx) {
+    auto go = [&](auto t, auto dd) {
+        return packed_simt<decltype(t), decltype(dd)::value>(q, k, v, cu, o, B, H, Hkv, total, scale, st, ctx);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (dt == DType::F32) return d == 64 ? go(float{}, D64{}) : go(float{}, D128{});
+    return d == 64 ? go(__nv_bfloat16{}, D64{}) : go(__nv_bfloat16{}, D128{});
+}
+
+cudaError_t launch_tree_simt(DType dt, KvFormat f, const void* q, const KvPages& pages,
+                             const uint64_t* masks, void* o, const int32_t* ctx_len, int max_ctx,
+                             int B, int H, int Hkv, int T, int d, float scale, void* ws,
+                             cudaStream_t st, DevCtx ctx) {
+    tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, H / Hkv * T, tree::row_tiles(H / Hkv * T, kRows), kKeys};
+    auto go2 = [&](auto t, auto dd) {
+        using E = decltype(t);
+        constexpr int D = decltype(dd)::value;
+        if (f == KvFormat::Int8) return tree_simt<E, D, KvFormat::Int8>(q, pages, masks, o, s, ws, scale, st, ctx);
+        if (f == KvFormat::E4M3) return tree_simt<E, D, KvFormat::E4M3>(q, pages, masks, o, s, ws, scale, st, ctx);
+        return tree_simt<E, D, KvFormat::Same>(q, pages, masks, o, s, ws, scale, st, ctx);
+    };
+    using D64 = std::integral_constant<int, 64>;
+    using D128 = std::integral_constant<int, 128>;
+    if (dt == DType::F32) return d == 64 ? go2(float{}, D64{}) : go2(float{}, D128{});
+    return d == 64 ? go2(__nv_bfloat16{}, D64{}) : go2(__nv_bfloat16{}, D128{});
+}
+
+}  // namespace sala

@@ -179,6 +179,42 @@ cudaError_t launch_qk_prologue(DType dt, const void* q, void* q_out, int64_t q_r
                                void* k_out, int64_t k_rows, int d, float eps, int N, int64_t pos0,
                                double rope_base, cudaStream_t st);
 
+// Dense softmax attention of the serving path: packed prompts, and drafted tokens over a paged
+// key/value cache, which may hold 8-bit codes with one fp32 scale per row (token and KV head).
+enum class KvFormat { Same = SALA_KV_SAME, Int8 = SALA_KV_INT8, E4M3 = SALA_KV_E4M3 };
+struct KvPages {
+    const void* k;         // [n_pages][Hkv][64][d] elements or codes
+    const void* v;
+    const float* k_scale;  // [n_pages][Hkv][64], 8-bit formats
+    const float* v_scale;
+    const int32_t* table;  // [B][max_pages]
+    int max_pages, n_pages;
+};
+namespace tree {
+struct Shape;
+struct Partials;
+}
+cudaError_t launch_kv_write(DType dt, KvFormat f, const void* k, const void* v, const int32_t* cu,
+                            const int32_t* pos, const KvPages& p, int B, int Hkv, int total, int d,
+                            cudaStream_t st, DevCtx ctx);
+cudaError_t launch_kv_read(DType dt, KvFormat f, const KvPages& p, const int32_t* cu, const int32_t* pos,
+                           void* k, void* v, int B, int Hkv, int total, int d, cudaStream_t st,
+                           DevCtx ctx);
+cudaError_t launch_packed_simt(DType dt, const void* q, const void* k, const void* v,
+                               const int32_t* cu, void* o, int B, int H, int Hkv, int total, int d,
+                               float scale, cudaStream_t st, DevCtx ctx);
+// ws: tree_simt_workspace(d) bytes.
+size_t tree_simt_workspace(int d);
+int tree_simt_ctas();
+cudaError_t launch_tree_simt(DType dt, KvFormat f, const void* q, const KvPages& pages,
+                             const uint64_t* masks, void* o, const int32_t* ctx_len, int max_ctx,
+                             int B, int H, int Hkv, int T, int d, float scale, void* ws,
+                             cudaStream_t st, DevCtx ctx);
+// Adds up the partials that the attention kernel's CTAs left (launched as its programmatic
+// dependent: it waits for that kernel before it reads anything).
+cudaError_t launch_tree_join(DType dt, const tree::Partials& part, void* out, const tree::Shape& s,
+                             int rt, int d, int n_cta, cudaStream_t st);
+
 // Diagnostics.
 cudaError_t launch_selftest_wait(cudaStream_t st, DevCtx ctx);
 

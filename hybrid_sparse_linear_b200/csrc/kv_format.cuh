@@ -1,0 +1,121 @@
+// The paged key/value cache of the dense serving path: its formats, page lookup and element
+// conversions, and the row ranges of packed sequences.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "kernels.h"
+
+namespace sala {
+
+constexpr int kPage = 64;  // tokens per page
+
+// Page of block j of sequence b, or -1 when the table has no such entry or names no page.
+__device__ __forceinline__ int page_of(const KvPages& p, int b, int j) {
+    if (j < 0 || j >= p.max_pages) return -1;
+    const int id = __ldg(p.table + (int64_t)b * p.max_pages + j);
+    return id >= 0 && id < p.n_pages ? id : -1;
+}
+
+// Quantisation of a row from its largest magnitude a (floored at 2^-100, so that scale and
+// reciprocal stay normal numbers).
+//   Int8: scale = a / 127, mul = 127 / a, code = the integer nearest to x * mul, ties to even.
+//         The product is formed and rounded to an integer in one fused operation, so no second
+//         rounding sits next to a border.
+//   E4M3: scale = the smallest power of two with a / scale <= 448, mul = its inverse.  e4m3 has
+//         its precision relative to each value, so a power of two costs none (down to the type's
+//         subnormals) and x * mul and code * scale are exact.
+struct RowScale {
+    float scale, mul;
+};
+template <KvFormat F>
+__device__ __forceinline__ RowScale row_scale(float a) {
+    a = fmaxf(a, 7.8886090522101181e-31f);  // 2^-100
+    if constexpr (F == KvFormat::Int8) {
+        return {__fdiv_rn(a, 127.f), __fdiv_rn(127.f, a)};
+    } else {
+        // a = m 2^e with m in [1, 2): a / 2^k <= 448 = 1.75 * 2^8 takes k = e - 8, one more above 1.75
+        const uint32_t u = __float_as_uint(a);
+        const int k = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+        return {__uint_as_float((uint32_t)(127 + k) << 23), __uint_as_float((uint32_t)(127 - k) << 23)};
+    }
+}
+// Codes of four values, in memory order.
+template <KvFormat F>
+__device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float x3, float mul) {
+    if constexpr (F == KvFormat::Int8) {
+        constexpr float kShift = 12582912.f;  // 1.5 * 2^23: the integer lands in the low mantissa bits
+        const uint32_t c0 = __float_as_uint(fmaf(x0, mul, kShift)), c1 = __float_as_uint(fmaf(x1, mul, kShift));
+        const uint32_t c2 = __float_as_uint(fmaf(x2, mul, kShift)), c3 = __float_as_uint(fmaf(x3, mul, kShift));
+        return __byte_perm(__byte_perm(c0, c1, 0x0040), __byte_perm(c2, c3, 0x0040), 0x5410);
+    } else {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x0 * mul, x1 * mul), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x2 * mul, x3 * mul), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    }
+}
+// The four code values (without the scale).
+template <KvFormat F>
+__device__ __forceinline__ float4 decode4(uint32_t c) {
+    if constexpr (F == KvFormat::Int8) {
+        return make_float4((float)(int8_t)c, (float)(int8_t)(c >> 8), (float)(int8_t)(c >> 16),
+                           (float)(int8_t)(c >> 24));
+    } else {
+        const __half2 lo(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3));
+        const __half2 hi(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3));
+        const float2 a = __half22float2(lo), b = __half22float2(hi);
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+}
+
+// ---------------------------------------------------------------- packed sequences
+// Rows cu[b] .. cu[b + 1] of a packed tensor belong to sequence b.  A pair of offsets that does not
+// lie in order inside [0, total] counts as an empty sequence and sets *bad.
+__device__ __forceinline__ int packed_len(const int32_t* cu, int b, int total, int* start, bool* bad) {
+    const int s = __ldg(cu + b), e = __ldg(cu + b + 1);
+    *start = s;
+    if (s < 0 || e < s || e > total) {
+        *bad = true;
+        return 0;
+    }
+    return e - s;
+}
+
+// The i-th tile of `rows` rows over all sequences, each sequence's tiles from its end to its start
+// (the longest causal rows first).  len = 0: there is no such tile.  By one converged warp.
+struct PackedTile {
+    int start, len, first;  // the sequence's rows, and the tile's first row inside it
+};
+__device__ __forceinline__ PackedTile find_packed_tile(const int32_t* cu, int B, int total, int64_t i,
+                                                       int rows, int lane, const DevCtx& ctx,
+                                                       bool report) {
+    int64_t before = 0;
+    bool bad = false;
+    PackedTile t{0, 0, 0};
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int b = b0 + lane;
+        int start = 0;
+        const int len = b < B ? packed_len(cu, b, total, &start, &bad) : 0;
+        const int n = (len + rows - 1) / rows;
+        int64_t inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + inc > i);
+        if (hit && t.len == 0) {
+            const int w = __ffs((int)hit) - 1;
+            t.start = __shfl_sync(0xffffffffu, start, w);
+            t.len = __shfl_sync(0xffffffffu, len, w);
+            const int64_t end = __shfl_sync(0xffffffffu, before + inc, w);
+            t.first = (int)(end - 1 - i) * rows;
+            if (!report) return t;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (report && __any_sync(0xffffffffu, bad) && lane == 0) flag(ctx, kStatusBounds);
+    return t;
+}
+
+}  // namespace sala

@@ -1,0 +1,149 @@
+// How the attention of drafted tokens over a paged cache divides its work, shared by the
+// tensor-core kernel, the fp32 kernel and the kernel that joins their partial results.
+//
+// An item is (sequence b, KV head g, row tile rt): up to RT of the G * T query rows of the group
+// against all keys of the sequence, tiles(b) = ceil((ctx_b + T) / KT) key tiles long.  Laid end to
+// end (b outermost, then g, then rt), the items form one line of W tiles, and CTA c of n takes the
+// tiles [W c / n, W (c + 1) / n): every CTA has the same number of tiles, however ragged the
+// contexts are, and no host-side knowledge of them is needed.  A CTA whose run covers an item
+// whole writes the result; else it leaves a partial (row maximum, row sum, unnormalised output)
+// in one of its two slots -- slot 0 for the item its run begins in, slot 1 for a later one -- and
+// the join kernel, which redoes the same arithmetic, adds up the partials in CTA order.
+#pragma once
+
+#include "common.cuh"
+
+namespace sala {
+namespace tree {
+
+struct Shape {
+    const int32_t* ctx;  // [B] context lengths
+    int B, Hkv, G, T, max_ctx;
+    int rows;            // G * T query rows per (b, g)
+    int n_rt;            // row tiles per (b, g)
+    int kt;              // keys per tile
+};
+
+__host__ __device__ __forceinline__ int row_tiles(int rows, int rt) { return (rows + rt - 1) / rt; }
+
+// Context length of sequence b, clamped to [0, max_ctx] (a value outside is flagged by the caller
+// that passes bad).
+__device__ __forceinline__ int ctx_of(const Shape& s, int b, bool* bad = nullptr) {
+    const int c = __ldg(s.ctx + b);
+    if (c < 0 || c > s.max_ctx) {
+        if (bad) *bad = true;
+        return c < 0 ? 0 : s.max_ctx;
+    }
+    return c;
+}
+__device__ __forceinline__ int tiles_of(const Shape& s, int ctx) { return (ctx + s.T + s.kt - 1) / s.kt; }
+
+// W, by one converged warp (every lane gets it).
+__device__ __forceinline__ long long total_tiles(const Shape& s, int lane, bool* bad) {
+    long long w = 0;
+    for (int b = lane; b < s.B; b += 32) w += tiles_of(s, ctx_of(s, b, bad));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    return w * s.Hkv * s.n_rt;
+}
+
+__device__ __forceinline__ long long run_start(long long w, int c, int n) { return w * c / n; }
+// The CTA whose run holds tile x (0 <= x < w).
+__device__ __forceinline__ int run_of(long long w, long long x, int n) {
+    return (int)(((x + 1) * n - 1) / w);  // the last c with floor(w c / n) <= x
+}
+
+// One item and the part of it that a run covers.
+struct Cursor {
+    int b, g, rt;
+    int ctx, n_tiles;    // of sequence b
+    int tile;            // first tile of the item inside the run
+    long long left;      // tiles of the run from here on
+};
+
+// The position of tile x of the line, by one converged warp; left is the run's length.
+__device__ __forceinline__ Cursor find_tile(const Shape& s, long long x, long long left, int lane) {
+    Cursor c;
+    c.left = left;
+    const long long per = (long long)s.Hkv * s.n_rt;
+    long long before = 0;
+    for (int b0 = 0; b0 < s.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int ctx = b < s.B ? ctx_of(s, b) : 0;
+        long long n = b < s.B ? tiles_of(s, ctx) * per : 0, inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += up;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, b < s.B && before + inc > x);
+        if (hit) {
+            const int w = __ffs((int)hit) - 1;
+            const long long start = __shfl_sync(0xffffffffu, before + inc - n, w);
+            c.ctx = __shfl_sync(0xffffffffu, ctx, w);
+            c.b = b0 + w;
+            c.n_tiles = tiles_of(s, c.ctx);
+            const long long r = x - start;
+            const int item = (int)(r / c.n_tiles);
+            c.tile = (int)(r - (long long)item * c.n_tiles);
+            c.g = item / s.n_rt;
+            c.rt = item - c.g * s.n_rt;
+            return c;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    c.b = s.B;  // past the end
+    c.g = c.rt = c.ctx = c.tile = 0;
+    c.n_tiles = 1;
+    c.left = 0;
+    return c;
+}
+
+// Tiles of the cursor's item inside the run.
+__device__ __forceinline__ int run_tiles(const Cursor& c) {
+    const long long n = c.n_tiles - c.tile;
+    return (int)(n < c.left ? n : c.left);
+}
+
+__device__ __forceinline__ void next_item(const Shape& s, Cursor& c) {
+    c.left -= run_tiles(c);
+    c.tile = 0;
+    if (++c.rt == s.n_rt) {
+        c.rt = 0;
+        if (++c.g == s.Hkv) {
+            c.g = 0;
+            ++c.b;
+            if (c.left > 0 && c.b < s.B) {
+                c.ctx = ctx_of(s, c.b);
+                c.n_tiles = tiles_of(s, c.ctx);
+            } else {
+                c.left = 0;
+            }
+        }
+    }
+}
+
+// Bits of the drafts that row t of sequence b attends to.
+__device__ __forceinline__ uint64_t draft_bits(const uint64_t* masks, int b, int t, int T) {
+    const uint64_t m = __ldg(reinterpret_cast<const unsigned long long*>(masks) + (int64_t)b * T + t);
+    return T >= 64 ? m : m & ((1ull << T) - 1);
+}
+
+// Partials: per CTA and slot, rt rows of (maximum in scaled log2 units, sum), then rt rows of d.
+__host__ __device__ __forceinline__ size_t partial_rows(int n_cta, int rt) { return (size_t)n_cta * 2 * rt; }
+struct Partials {
+    float2* ml;
+    float* o;
+};
+__host__ __device__ __forceinline__ size_t partial_bytes(int n_cta, int rt, int d) {
+    return partial_rows(n_cta, rt) * (sizeof(float2) + (size_t)d * sizeof(float));
+}
+inline Partials partials_at(void* ws, int n_cta, int rt) {
+    Partials p;
+    p.ml = static_cast<float2*>(ws);
+    p.o = reinterpret_cast<float*>(p.ml + partial_rows(n_cta, rt));
+    return p;
+}
+
+}  // namespace tree
+}  // namespace sala

@@ -7,6 +7,7 @@ library is missing this module fails to import.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -26,6 +27,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS = range(6)
 F32, BF16 = 0, 1
+KV_SAME, KV_INT8, KV_E4M3 = range(3)
 
 _vp, _i, _st = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _lib.sala_linear_prefill.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]
@@ -70,6 +72,13 @@ _lib.sala_sparse_prefill_lse.argtypes = [_vp] * 7 + [_i] * 7 + [ctypes.c_float, 
 _lib.sala_sparse_backward_workspace.argtypes = [_i] * 6
 _lib.sala_sparse_backward_workspace.restype = _st
 _lib.sala_sparse_backward.argtypes = [_vp] * 11 + [_i] * 7 + [ctypes.c_float, _vp, _st, _i, _vp]
+_lib.sala_packed_prefill.argtypes = [_vp] * 5 + [_i] * 5 + [ctypes.c_float, _i, _vp]
+_lib.sala_kv_write.argtypes = [_vp] * 5 + [_i] + [_vp] * 4 + [_i] * 8 + [_vp]
+_lib.sala_kv_read.argtypes = [_vp] * 4 + [_i, _vp, _i] + [_vp] * 4 + [_i] * 7 + [_vp]
+_lib.sala_tree_decode_paged.argtypes = [_vp] * 5 + [_i, _vp, _i, _vp, _i, _vp, _vp] + [_i] * 6 + [
+    ctypes.c_float, _vp, _st, _i, _i, _vp]
+_lib.sala_tree_decode_paged_workspace.argtypes = [_i] * 6
+_lib.sala_tree_decode_paged_workspace.restype = _st
 _lib.sala_check_status.argtypes = [_vp]
 _lib.sala_debug_bounds_build.restype = _i
 _lib.sala_status_string.argtypes = [_i]
@@ -82,6 +91,7 @@ for _f in ("sala_linear_prefill", "sala_linear_decode", "sala_linear_prefill_rop
            "sala_linear_backward", "sala_qk_norm", "sala_sparse_prefill_lse", "sala_sparse_backward",
            "sala_block_topk_qblock_softmax", "sala_linear_decode_pdl", "sala_qk_prologue",
            "sala_block_topk_per_head", "sala_sparse_prefill_per_head",
+           "sala_packed_prefill", "sala_kv_write", "sala_kv_read", "sala_tree_decode_paged",
            "sala_block_compress",
            "sala_block_topk",
            "sala_sparse_prefill", "sala_sparse_decode", "sala_sparse_decode_pdl", "sala_check_status",
@@ -489,6 +499,166 @@ def sparse_decode_paged(q, k_pages, v_pages, page_table, kbar, pos, max_pos, top
                                          _ptr(o), B, H, Hkv, d, 64, topk, n_init, n_local,
                                          ctypes.c_float(scale), _ptr(workspace), workspace.numel(),
                                          _dt(q), _stream(stream)), "sala_sparse_decode_paged")
+    return o
+
+
+# ----------------------------------------------------------------------------------------------
+# Dense serving path: packed prompts, the paged cache, and new or drafted tokens over it
+
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on(t, stream, *others):
+    """Context in which a call on t's device allocates and launches: the given stream (whose pool
+    then owns what the call allocates), else t's device's current stream.  Every tensor of the call
+    has to lie on that device."""
+    for x in others:
+        if x is not None and x.device != t.device:
+            raise ValueError(f"tensors on {t.device} and {x.device}")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream on {stream.device}, tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index != torch.cuda.current_device():
+        return torch.cuda.stream(torch.cuda.current_stream(t.device))
+    return _NO_SWITCH
+
+
+def _need_offsets(cu_seqlens):
+    _need(cu_seqlens, "cu_seqlens", dtype=torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected (B + 1,)")
+    return cu_seqlens.shape[0] - 1
+
+
+_KV_FORMATS = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}
+
+
+def _need_pages(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype):
+    """Checks the page pool; returns (n_pages, Hkv, d, format)."""
+    _need(k_pages, "k_pages")
+    if k_pages.dim() != 4 or k_pages.shape[2] != 64:
+        raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, expected (n_pages, Hkv, 64, d)")
+    _need(v_pages, "v_pages", k_pages.shape, k_pages.dtype)
+    _need(page_table, "page_table", dtype=torch.int32)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, max_pages)")
+    fmt = _KV_FORMATS.get(k_pages.dtype, KV_SAME)
+    if fmt == KV_SAME:
+        if k_pages.dtype != dtype:
+            raise ValueError(f"k_pages has dtype {k_pages.dtype}, expected {dtype}, int8 or float8_e4m3fn")
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to int8 and float8_e4m3fn pages")
+    else:
+        for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if s is None:
+                raise ValueError(f"{n} is needed for {k_pages.dtype} pages")
+            _need(s, n, k_pages.shape[:3], torch.float32)
+    return k_pages.shape[0], k_pages.shape[1], k_pages.shape[3], fmt
+
+
+def packed_prefill(q, k, v, cu_seqlens, o=None, scale=0.0, stream=None):
+    """Causal softmax attention over B prompts of different lengths laid one behind the other.
+    q: [H, total, d]; k, v: [Hkv, total, d]; cu_seqlens: [B + 1] int32 row offsets (device).
+    Rows behind cu_seqlens[B] of o are left as they were.  Returns o.  Forward only."""
+    _need(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected (H, total, d)")
+    H, total, d = q.shape
+    _need(k, "k", dtype=q.dtype)
+    if k.dim() != 3 or k.shape[1:] != q.shape[1:]:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected (Hkv, {total}, {d})")
+    _need(v, "v", k.shape, q.dtype)
+    B = _need_offsets(cu_seqlens)
+    _need(o, "o", q.shape, q.dtype)
+    with _on(q, stream, k, v, cu_seqlens, o):
+        if o is None:
+            o = torch.empty_like(q)
+        _check(_lib.sala_packed_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(o), B, H,
+                                        k.shape[0], total, d, float(scale), _dt(q), _stream(stream)),
+               "sala_packed_prefill")
+    return o
+
+
+def kv_write(k, v, cu_seqlens, pos, page_table, k_pages, v_pages, k_scale=None, v_scale=None,
+             stream=None):
+    """Writes packed rows k, v [Hkv, total, d] into the paged cache: row cu_seqlens[b] + i becomes
+    token pos[b] + i of sequence b (cu_seqlens [B + 1], pos [B], page_table [B, max_pages] int32).
+    k_pages, v_pages: [n_pages, Hkv, 64, d] of k's dtype, int8 or float8_e4m3fn; the 8-bit types
+    take a scale per row in k_scale, v_scale [n_pages, Hkv, 64] fp32."""
+    _need(k, "k")
+    if k.dim() != 3:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected (Hkv, total, d)")
+    _need(v, "v", k.shape, k.dtype)
+    B = _need_offsets(cu_seqlens)
+    _need(pos, "pos", (B,), torch.int32)
+    n_pages, Hkv, d, fmt = _need_pages(k_pages, v_pages, page_table, k_scale, v_scale, B, k.dtype)
+    if (k.shape[0], k.shape[2]) != (Hkv, d):
+        raise ValueError(f"k has shape {tuple(k.shape)}, the pages hold ({Hkv}, tokens, {d})")
+    with _on(k, stream, v, cu_seqlens, pos, page_table, k_pages, v_pages, k_scale, v_scale):
+        _check(_lib.sala_kv_write(_ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(pos), _ptr(page_table),
+                                  page_table.shape[1], _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                                  _ptr(v_scale), n_pages, B, Hkv, k.shape[1], d, 64, fmt, _dt(k),
+                                  _stream(stream)), "sala_kv_write")
+
+
+def kv_read(k_pages, v_pages, page_table, cu_seqlens, pos, total, dtype, k_scale=None, v_scale=None,
+            k=None, v=None, stream=None):
+    """Reads tokens pos[b] .. of each sequence back as packed rows of dtype, cu_seqlens[b + 1] -
+    cu_seqlens[b] of them: the inverse of kv_write.  Returns (k, v), [Hkv, total, d] each; rows
+    behind cu_seqlens[B] are left as they were."""
+    B = _need_offsets(cu_seqlens)
+    _need(pos, "pos", (B,), torch.int32)
+    n_pages, Hkv, d, fmt = _need_pages(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype)
+    _need(k, "k", (Hkv, total, d), dtype)
+    _need(v, "v", (Hkv, total, d), dtype)
+    with _on(k_pages, stream, v_pages, page_table, cu_seqlens, pos, k_scale, v_scale, k, v):
+        if k is None:
+            k = torch.empty((Hkv, total, d), dtype=dtype, device=k_pages.device)
+        if v is None:
+            v = torch.empty((Hkv, total, d), dtype=dtype, device=k_pages.device)
+        _check(_lib.sala_kv_read(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), n_pages,
+                                 _ptr(page_table), page_table.shape[1], _ptr(cu_seqlens), _ptr(pos),
+                                 _ptr(k), _ptr(v), B, Hkv, total, d, 64, fmt, _dt(k),
+                                 _stream(stream)), "sala_kv_read")
+    return k, v
+
+
+def tree_decode_paged_workspace_bytes(B, H, Hkv, T, max_ctx, d):
+    return _lib.sala_tree_decode_paged_workspace(B, H, Hkv, T, max_ctx, d)
+
+
+def tree_decode_paged(q, k_pages, v_pages, page_table, ctx, max_ctx, tree, k_scale=None, v_scale=None,
+                      o=None, scale=0.0, workspace=None, stream=None):
+    """Attention of T new tokens per sequence (T = 1: a decode step; T <= 64: a tree of drafts) over
+    the paged cache, which holds ctx[b] tokens of context and the T new ones behind them.
+    q: [B, H, T, d]; ctx [B] int32, each <= max_ctx; tree [B, T] int64, bit j of row t set when new
+    token t attends to new token j.  Pages and scales as in kv_write.  Returns o [B, H, T, d]."""
+    _need(q, "q")
+    if q.dim() != 4:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected (B, H, T, d)")
+    B, H, T, d = q.shape
+    n_pages, Hkv, dp, fmt = _need_pages(k_pages, v_pages, page_table, k_scale, v_scale, B, q.dtype)
+    if dp != d:
+        raise ValueError(f"q has head dim {d}, the pages {dp}")
+    if not 0 <= int(max_ctx) < 1 << 31:
+        raise ValueError(f"max_ctx {max_ctx} outside [0, 2^31)")
+    _need(ctx, "ctx", (B,), torch.int32)
+    _need(tree, "tree", (B, T), torch.int64)
+    _need(o, "o", q.shape, q.dtype)
+    _need(workspace, "workspace", dtype=torch.uint8)
+    with _on(q, stream, k_pages, v_pages, page_table, ctx, tree, k_scale, v_scale, o, workspace):
+        if o is None:
+            o = torch.empty_like(q)
+        if workspace is None:
+            need = _lib.sala_tree_decode_paged_workspace(B, H, Hkv, T, int(max_ctx), d)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        _check(_lib.sala_tree_decode_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                                           _ptr(v_scale), n_pages, _ptr(page_table),
+                                           page_table.shape[1], _ptr(ctx), int(max_ctx), _ptr(tree),
+                                           _ptr(o), B, H, Hkv, T, d, 64, float(scale),
+                                           _ptr(workspace), workspace.numel(), fmt, _dt(q),
+                                           _stream(stream)), "sala_tree_decode_paged")
     return o
 
 

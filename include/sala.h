@@ -51,6 +51,10 @@ typedef enum {
 
 typedef enum { SALA_F32 = 0, SALA_BF16 = 1 } sala_dtype;
 
+/* What the pages of a key/value cache hold: elements of the call's dt, or 8-bit codes with one
+ * fp32 scale per row (see sala_kv_write). */
+typedef enum { SALA_KV_SAME = 0, SALA_KV_INT8 = 1, SALA_KV_E4M3 = 2 } sala_kv_format;
+
 typedef void* sala_stream; /* a cudaStream_t */
 
 /* ------------------------------------------------------------------------------------------
@@ -477,6 +481,85 @@ sala_status sala_sparse_decode_noalloc(const void* q, const void* kcache, const 
                                        int nb_cap, int d, int block, int topk, int n_init,
                                        int n_local, float scale, sala_dtype dt,
                                        sala_stream stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Dense serving path: whole prompts of different lengths in one call, a paged key/value cache that
+ * may be held in 8 bits, and the attention of new or drafted tokens over it.  The pages describe
+ * no serving system; these are the plain operators a server needs next to the layers above.
+ *
+ * Packed tensors hold the rows of B sequences one behind the other: [heads, total, d], sequence b
+ * in rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of every head (cu_seqlens: [B + 1] int32 device,
+ * ascending from 0, at most total; equal neighbours are an empty sequence).  Rows behind the last
+ * sequence are neither read into any result nor written.  Offsets out of order are flagged
+ * (SALA_ERR_BOUNDS through sala_check_status) and the rows they leave unclear are skipped.
+ *
+ * Pages hold 64 tokens of one sequence for every KV head: k_pages, v_pages [n_pages, Hkv, 64, d],
+ * in the 8-bit formats with k_scale, v_scale [n_pages, Hkv, 64] fp32 (NULL otherwise).
+ * page_table [B, max_pages] int32 device: entry [b][j] is the page of the tokens 64 j .. 64 j + 63
+ * of sequence b.  An entry outside [0, n_pages) where one is needed is flagged (SALA_ERR_BOUNDS)
+ * and what it should hold is left out.  Slots behind a sequence's last token may hold anything.
+ */
+
+/* Causal softmax attention over packed prompts:
+ *   o_i = sum_{j} softmax_j(scale q_i . k_j) v_j  over the keys j <= i of row i's sequence.
+ * q, o : [H, total, d] device, dt.   k, v : [Hkv, total, d] device, dt.   H a multiple of Hkv.
+ * d    : 64 or 128.  scale: 0 selects 1/sqrt(d); finite and >= 0.
+ * A row's result depends on the rows it attends to alone: an infinity or a NaN in a later token or
+ * in another sequence does not reach it. */
+sala_status sala_packed_prefill(const void* q, const void* k, const void* v,
+                                const int32_t* cu_seqlens, void* o, int B, int H, int Hkv,
+                                int total, int d, float scale, sala_dtype dt, sala_stream stream);
+
+/* Writes packed key and value rows into the cache: row cu_seqlens[b] + i becomes token pos[b] + i
+ * of sequence b.  In the 8-bit formats each row (one token of one KV head, d values, largest
+ * magnitude a, taken as at least 2^-100) is held as codes and one fp32 scale, its values read back
+ * as code * scale:
+ *   SALA_KV_INT8 : scale = a / 127, code = the integer nearest to x * (127 / a), ties to even
+ *   SALA_KV_E4M3 : scale = the smallest power of two with a / scale <= 448, code = e4m3(x / scale),
+ *                  round to nearest even (both x / scale and code * scale are exact)
+ * A row that holds an infinity or a NaN gets the scale NaN and codes 0, so that every use of it
+ * gives NaN.  SALA_KV_SAME copies the rows.
+ * k, v       : [Hkv, total, d] device, dt.   pos : [B] int32 device, >= 0.
+ * block      : 64 (tokens per page).   d : 64 or 128.
+ * Two rows written to one slot by one call leave either of them, or a mix: give each token once. */
+sala_status sala_kv_write(const void* k, const void* v, const int32_t* cu_seqlens,
+                          const int32_t* pos, const int32_t* page_table, int max_pages,
+                          void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                          int n_pages, int B, int Hkv, int total, int d, int block,
+                          sala_kv_format fmt, sala_dtype dt, sala_stream stream);
+
+/* Reads tokens pos[b] .. of each sequence back as packed rows (the inverse of sala_kv_write:
+ * token pos[b] + i of sequence b becomes row cu_seqlens[b] + i), each value code * scale in 32
+ * bits, rounded once to dt.  A row whose page the table does not hold is left as it was.
+ * k, v : [Hkv, total, d] device, dt.  Other arguments as sala_kv_write. */
+sala_status sala_kv_read(const void* k_pages, const void* v_pages, const float* k_scale,
+                         const float* v_scale, int n_pages, const int32_t* page_table,
+                         int max_pages, const int32_t* cu_seqlens, const int32_t* pos, void* k,
+                         void* v, int B, int Hkv, int total, int d, int block, sala_kv_format fmt,
+                         sala_dtype dt, sala_stream stream);
+
+/* Attention of T new tokens per sequence over the paged cache: the step that verifies a tree of
+ * drafted tokens, and with T = 1 the plain decode step.  Sequence b's cache holds ctx[b] tokens of
+ * context and behind them the T new ones (written there by sala_kv_write).  Row t attends to the
+ * whole context and to the new token j exactly when bit j of tree[b][t] is set; for a tree of
+ * drafts those are the bits of its ancestors and its own.  A row that attends to nothing gives 0.
+ * q, o       : [B, H, T, d] device, dt.   1 <= T <= 64.
+ * ctx        : [B] int32 device, each in [0, max_ctx] (outside: flagged and clamped).
+ * max_ctx    : the largest context, max_ctx + T <= max_pages * 64.
+ * tree       : [B, T] uint64 device; bits at and above T are ignored.
+ * scale      : 0 selects 1/sqrt(d); finite and >= 0.   d : 64 or 128.   block : 64.
+ * workspace  : at least sala_tree_decode_paged_workspace(...) bytes of device scratch, 16-byte
+ *              aligned, no initial value needed, not shared with a concurrent call.
+ * The sums over the keys are split over the SMs and joined in a fixed order: equal inputs give
+ * equal bits.  An infinity or a NaN in a new token reaches the rows that attend to it alone. */
+sala_status sala_tree_decode_paged(const void* q, const void* k_pages, const void* v_pages,
+                                   const float* k_scale, const float* v_scale, int n_pages,
+                                   const int32_t* page_table, int max_pages, const int32_t* ctx,
+                                   int max_ctx, const uint64_t* tree, void* o, int B, int H,
+                                   int Hkv, int T, int d, int block, float scale, void* workspace,
+                                   size_t workspace_bytes, sala_kv_format fmt, sala_dtype dt,
+                                   sala_stream stream);
+size_t sala_tree_decode_paged_workspace(int B, int H, int Hkv, int T, int max_ctx, int d);
 
 /* ------------------------------------------------------------------------------------------
  * Status and diagnostics. */
