@@ -914,10 +914,13 @@ sala_status sala_packed_prefill(const void* q, const void* k, const void* v,
     if (scale == 0.f) scale = 1.0f / sqrtf((float)d);
     sala::DevCtx ctx;
     if ((s = get_ctx(&ctx)) != SALA_OK) return s;
-    const cudaError_t e = sala::launch_packed_simt(to_dt(dt), q, k, v, cu_seqlens, o, B, H, Hkv,
-                                                   total, d, scale, static_cast<cudaStream_t>(stream), ctx);
-    if (e == cudaErrorNotSupported) return fail(SALA_ERR_UNSUPPORTED, "more than 65535 query heads");
-    return launched(e, "packed_prefill");
+    REQUIRE(H <= 65535, SALA_ERR_UNSUPPORTED, "H %d above 65535", H);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dt == SALA_BF16)
+        return launched(sala::launch_packed_tc(q, k, v, cu_seqlens, o, B, H, Hkv, total, d, scale, st, ctx),
+                        "packed_prefill_tc");
+    return launched(sala::launch_packed_simt(q, k, v, cu_seqlens, o, B, H, Hkv, total, d, scale, st, ctx),
+                    "packed_prefill");
 }
 
 sala_status sala_kv_write(const void* k, const void* v, const int32_t* cu_seqlens,

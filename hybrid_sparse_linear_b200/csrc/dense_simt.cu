@@ -170,10 +170,10 @@ __device__ __forceinline__ float4 kv_load4(const void* p, const float* scale, in
 // ---------------------------------------------------------------- packed prompts
 // Block = (64 consecutive tokens of one sequence, one query head); blockIdx.x counts the tiles of
 // all sequences, an upper bound of which the host launches.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, 2)
-packed_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-                   const int32_t* __restrict__ cu, T* __restrict__ out, int B, int H, int Hkv,
+packed_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                   const int32_t* __restrict__ cu, float* __restrict__ out, int B, int H, int Hkv,
                    int total, float sl2, DevCtx ctx) {
     extern __shared__ __align__(16) float sm[];
     __shared__ PackedTile tile;
@@ -188,8 +188,8 @@ packed_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     if (t.len <= 0) return;
     const int h = blockIdx.y, kvh = h / (H / Hkv);
     const int64_t row0 = (int64_t)h * total + t.start + t.first;
-    const T* kb = k + ((int64_t)kvh * total + t.start) * D;
-    const T* vb = v + ((int64_t)kvh * total + t.start) * D;
+    const float* kb = k + ((int64_t)kvh * total + t.start) * D;
+    const float* vb = v + ((int64_t)kvh * total + t.start) * D;
     const int n_rows = min(kRows, t.len - t.first);
     constexpr int kLd = D + kPad;
     for (int e = tid; e < kRows * (D / 4); e += kThreads) {
@@ -202,7 +202,7 @@ packed_simt_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
     for (int k0 = 0; k0 <= t.first; k0 += kKeys) {
         const bool masked = k0 + kKeys > t.first;
         const int n_keys = min(kKeys, t.len - k0);
-        auto load = [&](const T* base, int r, int c) {
+        auto load = [&](const float* base, int r, int c) {
             return r < n_keys ? load4(base + (int64_t)(k0 + r) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         };
         attend_tile<D>(st, sm, sl2, masked, [&](int r, int c) { return load(kb, r, c); },
@@ -298,17 +298,16 @@ tree_simt_kernel(const T* __restrict__ q, KvPages pages, const uint64_t* __restr
     }
 }
 
-template <typename T, int D>
+template <int D>
 cudaError_t packed_simt(const void* q, const void* k, const void* v, const int32_t* cu, void* o,
                         int B, int H, int Hkv, int total, float scale, cudaStream_t st, DevCtx ctx) {
     constexpr int bytes = smem_floats<D>() * 4;
-    if (cudaError_t e = ensure_smem<packed_simt_kernel<T, D>>(bytes); e != cudaSuccess) return e;
+    if (cudaError_t e = ensure_smem<packed_simt_kernel<D>>(bytes); e != cudaSuccess) return e;
     // every sequence has at most one tile that is not full
     const long long tiles = (long long)total / kRows + (B < total ? B : total);
-    if (H > 65535 || tiles > 0x7fffffffll) return cudaErrorNotSupported;
-    packed_simt_kernel<T, D><<<dim3((unsigned)tiles, H), kThreads, bytes, st>>>(
-        static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), cu,
-        static_cast<T*>(o), B, H, Hkv, total, scale * 1.4426950408889634f, ctx);
+    packed_simt_kernel<D><<<dim3((unsigned)tiles, H), kThreads, bytes, st>>>(
+        static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v), cu,
+        static_cast<float*>(o), B, H, Hkv, total, scale * 1.4426950408889634f, ctx);
     return cudaGetLastError();
 }
 
@@ -332,16 +331,11 @@ cudaError_t tree_simt(const void* q, const KvPages& pages, const uint64_t* masks
 int tree_simt_ctas() { return 2 * device_sm_count(); }
 size_t tree_simt_workspace(int d) { return tree::partial_bytes(tree_simt_ctas(), kRows, d); }
 
-cudaError_t launch_packed_simt(DType dt, const void* q, const void* k, const void* v,
-                               const int32_t* cu, void* o, int B, int H, int Hkv, int total, int d,
-                               float scale, cudaStream_t st, DevCtx ctx) {
-    auto go = [&](auto t, auto dd) {
-        return packed_simt<decltype(t), decltype(dd)::value>(q, k, v, cu, o, B, H, Hkv, total, scale, st, ctx);
-    };
-    using D64 = std::integral_constant<int, 64>;
-    using D128 = std::integral_constant<int, 128>;
-    if (dt == DType::F32) return d == 64 ? go(float{}, D64{}) : go(float{}, D128{});
-    return d == 64 ? go(__nv_bfloat16{}, D64{}) : go(__nv_bfloat16{}, D128{});
+cudaError_t launch_packed_simt(const void* q, const void* k, const void* v, const int32_t* cu, void* o,
+                               int B, int H, int Hkv, int total, int d, float scale, cudaStream_t st,
+                               DevCtx ctx) {
+    return d == 64 ? packed_simt<64>(q, k, v, cu, o, B, H, Hkv, total, scale, st, ctx)
+                   : packed_simt<128>(q, k, v, cu, o, B, H, Hkv, total, scale, st, ctx);
 }
 
 cudaError_t launch_tree_simt(DType dt, KvFormat f, const void* q, const KvPages& pages,

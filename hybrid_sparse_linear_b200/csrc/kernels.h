@@ -200,9 +200,14 @@ cudaError_t launch_kv_write(DType dt, KvFormat f, const void* k, const void* v, 
 cudaError_t launch_kv_read(DType dt, KvFormat f, const KvPages& p, const int32_t* cu, const int32_t* pos,
                            void* k, void* v, int B, int Hkv, int total, int d, cudaStream_t st,
                            DevCtx ctx);
-cudaError_t launch_packed_simt(DType dt, const void* q, const void* k, const void* v,
-                               const int32_t* cu, void* o, int B, int H, int Hkv, int total, int d,
-                               float scale, cudaStream_t st, DevCtx ctx);
+// fp32, on the CUDA cores.
+cudaError_t launch_packed_simt(const void* q, const void* k, const void* v, const int32_t* cu, void* o,
+                               int B, int H, int Hkv, int total, int d, float scale, cudaStream_t st,
+                               DevCtx ctx);
+// bf16, on the tensor cores.
+cudaError_t launch_packed_tc(const void* q, const void* k, const void* v, const int32_t* cu, void* o,
+                             int B, int H, int Hkv, int total, int d, float scale, cudaStream_t st,
+                             DevCtx ctx);
 // ws: tree_simt_workspace(d) bytes.
 size_t tree_simt_workspace(int d);
 int tree_simt_ctas();
