@@ -971,7 +971,10 @@ sala_status sala_kv_read(const void* k_pages, const void* v_pages, const float* 
 
 size_t sala_tree_decode_paged_workspace(int B, int H, int Hkv, int T, int max_ctx, int d) {
     if (B <= 0 || H <= 0 || Hkv <= 0 || T <= 0 || max_ctx < 0 || (d != 64 && d != 128)) return 0;
-    return (sala::tree_simt_workspace(d) + 255) & ~(size_t)255;
+    const int64_t rows = (int64_t)(H / Hkv) * T;
+    if (rows > 1 << 20) return 0;
+    const size_t f32 = sala::tree_simt_workspace((int)rows, d), bf16 = sala::tree_tc_workspace((int)rows, d);
+    return ((f32 > bf16 ? f32 : bf16) + 255) & ~(size_t)255;
 }
 
 sala_status sala_tree_decode_paged(const void* q, const void* k_pages, const void* v_pages,
@@ -995,6 +998,7 @@ sala_status sala_tree_decode_paged(const void* q, const void* k_pages, const voi
     REQUIRE((int64_t)B * Hkv <= 65535, SALA_ERR_UNSUPPORTED, "B * Hkv = %lld above 65535",
             (long long)B * Hkv);
     REQUIRE((int64_t)(H / Hkv) * T <= 1 << 20, SALA_ERR_UNSUPPORTED, "more than 2^20 rows per KV head");
+    REQUIRE((int64_t)B * H * T <= 0x7fffffffll, SALA_ERR_UNSUPPORTED, "more than 2^31 - 1 query rows");
     REQ_PTR(q); REQ_PTR(o);
     REQUIRE(ctx_len != nullptr && tree != nullptr && ((uintptr_t)tree & 7) == 0, SALA_ERR_INVALID_ARG,
             "ctx and tree must be device pointers (tree 8-byte aligned)");
@@ -1006,9 +1010,13 @@ sala_status sala_tree_decode_paged(const void* q, const void* k_pages, const voi
     sala::DevCtx ctx;
     if ((s = get_ctx(&ctx)) != SALA_OK) return s;
     const sala::KvPages p{k_pages, v_pages, k_scale, v_scale, page_table, max_pages, n_pages};
-    return launched(sala::launch_tree_simt(to_dt(dt), (sala::KvFormat)fmt, q, p, tree, o, ctx_len,
-                                           max_ctx, B, H, Hkv, T, d, scale, workspace,
-                                           static_cast<cudaStream_t>(stream), ctx),
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dt == SALA_BF16)
+        return launched(sala::launch_tree_tc((sala::KvFormat)fmt, q, p, tree, o, ctx_len, max_ctx, B, H, Hkv,
+                                             T, d, scale, workspace, st, ctx),
+                        "tree_decode_paged_tc");
+    return launched(sala::launch_tree_simt((sala::KvFormat)fmt, q, p, tree, o, ctx_len, max_ctx, B, H, Hkv,
+                                           T, d, scale, workspace, st, ctx),
                     "tree_decode_paged");
 }
 

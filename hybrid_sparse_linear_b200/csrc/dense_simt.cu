@@ -138,28 +138,14 @@ __device__ __forceinline__ void attend_tile(Rows<D>& st, float* sm, float sl2, b
     __syncthreads();  // the next tile writes KV and P
 }
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-    return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                       __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-}
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 __device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(ptx::pack_bf16x2(x.x, x.y), ptx::pack_bf16x2(x.z, x.w));
-}
 
 // Four values of row `row` of the cache's keys or values.
-template <typename T, KvFormat F>
+template <KvFormat F>
 __device__ __forceinline__ float4 kv_load4(const void* p, const float* scale, int64_t row, int d, int col) {
     if constexpr (F == KvFormat::Same) {
-        return load4(static_cast<const T*>(p) + row * d + col);
+        return load4(static_cast<const float*>(p) + row * d + col);
     } else {
         const float4 x = decode4<F>(__ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + row * d + col)));
         const float s = __ldg(scale + row);
@@ -224,10 +210,10 @@ packed_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, con
 }
 
 // ---------------------------------------------------------------- drafted tokens, paged cache
-template <typename T, int D, KvFormat F>
+template <int D, KvFormat F>
 __global__ void __launch_bounds__(kThreads, 2)
-tree_simt_kernel(const T* __restrict__ q, KvPages pages, const uint64_t* __restrict__ masks,
-                 T* __restrict__ out, tree::Shape s, tree::Partials part, float sl2, DevCtx ctx) {
+tree_simt_kernel(const float* __restrict__ q, KvPages pages, const uint64_t* __restrict__ masks,
+                 float* __restrict__ out, tree::Shape s, tree::Partials part, float sl2, DevCtx ctx) {
     extern __shared__ __align__(16) float sm[];
     __shared__ tree::Cursor cur0;
     __shared__ uint64_t bits[kRows];
@@ -269,7 +255,7 @@ tree_simt_kernel(const T* __restrict__ q, KvPages pages, const uint64_t* __restr
             const int n_keys = min(kKeys, c.ctx + s.T - k0);
             const int64_t base = ((int64_t)page * s.Hkv + c.g) * kKeys;
             auto load = [&](const void* p, const float* sc, int r, int col) {
-                return r < n_keys ? kv_load4<T, F>(p, sc, base + r, D, col) : make_float4(0.f, 0.f, 0.f, 0.f);
+                return r < n_keys ? kv_load4<F>(p, sc, base + r, D, col) : make_float4(0.f, 0.f, 0.f, 0.f);
             };
             attend_tile<D>(st, sm, sl2, k0 + kKeys > c.ctx,
                            [&](int r, int col) { return load(pages.k, pages.k_scale, r, col); },
@@ -280,7 +266,7 @@ tree_simt_kernel(const T* __restrict__ q, KvPages pages, const uint64_t* __restr
                            });
         }
         const bool whole = c.tile == 0 && n == c.n_tiles;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * kRows;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * min(s.rows, kRows);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = ty * 4 + i;
@@ -311,25 +297,27 @@ cudaError_t packed_simt(const void* q, const void* k, const void* v, const int32
     return cudaGetLastError();
 }
 
-template <typename T, int D, KvFormat F>
+// A partial slot holds a row tile, or the group's rows where they are fewer.
+int slot_rows(int rows) { return rows < kRows ? rows : kRows; }
+int tree_ctas() { return 2 * device_sm_count(); }
+
+template <int D, KvFormat F>
 cudaError_t tree_simt(const void* q, const KvPages& pages, const uint64_t* masks, void* o,
                       const tree::Shape& s, void* ws, float scale, cudaStream_t st, DevCtx ctx) {
     constexpr int bytes = smem_floats<D>() * 4;
-    if (cudaError_t e = ensure_smem<tree_simt_kernel<T, D, F>>(bytes); e != cudaSuccess) return e;
-    const int n_cta = tree_simt_ctas();
-    const tree::Partials part = tree::partials_at(ws, n_cta, kRows);
-    tree_simt_kernel<T, D, F><<<n_cta, kThreads, bytes, st>>>(
-        static_cast<const T*>(q), pages, masks, static_cast<T*>(o), s, part,
+    if (cudaError_t e = ensure_smem<tree_simt_kernel<D, F>>(bytes); e != cudaSuccess) return e;
+    const int n_cta = tree_ctas();
+    const tree::Partials part = tree::partials_at(ws, n_cta, slot_rows(s.rows));
+    tree_simt_kernel<D, F><<<n_cta, kThreads, bytes, st>>>(
+        static_cast<const float*>(q), pages, masks, static_cast<float*>(o), s, part,
         scale * 1.4426950408889634f, ctx);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    return launch_tree_join(std::is_same<T, float>::value ? DType::F32 : DType::BF16, part, o, s, kRows,
-                            D, n_cta, st);
+    return launch_tree_join(DType::F32, part, o, s, slot_rows(s.rows), D, n_cta, st);
 }
 
 }  // namespace
 
-int tree_simt_ctas() { return 2 * device_sm_count(); }
-size_t tree_simt_workspace(int d) { return tree::partial_bytes(tree_simt_ctas(), kRows, d); }
+size_t tree_simt_workspace(int rows, int d) { return tree::partial_bytes(tree_ctas(), slot_rows(rows), d); }
 
 cudaError_t launch_packed_simt(const void* q, const void* k, const void* v, const int32_t* cu, void* o,
                                int B, int H, int Hkv, int total, int d, float scale, cudaStream_t st,
@@ -338,22 +326,18 @@ cudaError_t launch_packed_simt(const void* q, const void* k, const void* v, cons
                    : packed_simt<128>(q, k, v, cu, o, B, H, Hkv, total, scale, st, ctx);
 }
 
-cudaError_t launch_tree_simt(DType dt, KvFormat f, const void* q, const KvPages& pages,
-                             const uint64_t* masks, void* o, const int32_t* ctx_len, int max_ctx,
-                             int B, int H, int Hkv, int T, int d, float scale, void* ws,
-                             cudaStream_t st, DevCtx ctx) {
-    tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, H / Hkv * T, tree::row_tiles(H / Hkv * T, kRows), kKeys};
-    auto go2 = [&](auto t, auto dd) {
-        using E = decltype(t);
+cudaError_t launch_tree_simt(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
+                             const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
+                             float scale, void* ws, cudaStream_t st, DevCtx ctx) {
+    const int rows = H / Hkv * T;
+    const tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, rows, tree::row_tiles(rows, kRows), kKeys};
+    auto go = [&](auto dd) {
         constexpr int D = decltype(dd)::value;
-        if (f == KvFormat::Int8) return tree_simt<E, D, KvFormat::Int8>(q, pages, masks, o, s, ws, scale, st, ctx);
-        if (f == KvFormat::E4M3) return tree_simt<E, D, KvFormat::E4M3>(q, pages, masks, o, s, ws, scale, st, ctx);
-        return tree_simt<E, D, KvFormat::Same>(q, pages, masks, o, s, ws, scale, st, ctx);
+        if (f == KvFormat::Int8) return tree_simt<D, KvFormat::Int8>(q, pages, masks, o, s, ws, scale, st, ctx);
+        if (f == KvFormat::E4M3) return tree_simt<D, KvFormat::E4M3>(q, pages, masks, o, s, ws, scale, st, ctx);
+        return tree_simt<D, KvFormat::Same>(q, pages, masks, o, s, ws, scale, st, ctx);
     };
-    using D64 = std::integral_constant<int, 64>;
-    using D128 = std::integral_constant<int, 128>;
-    if (dt == DType::F32) return d == 64 ? go2(float{}, D64{}) : go2(float{}, D128{});
-    return d == 64 ? go2(__nv_bfloat16{}, D64{}) : go2(__nv_bfloat16{}, D128{});
+    return d == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
 }
 
 }  // namespace sala

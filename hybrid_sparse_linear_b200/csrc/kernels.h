@@ -208,13 +208,16 @@ cudaError_t launch_packed_simt(const void* q, const void* k, const void* v, cons
 cudaError_t launch_packed_tc(const void* q, const void* k, const void* v, const int32_t* cu, void* o,
                              int B, int H, int Hkv, int total, int d, float scale, cudaStream_t st,
                              DevCtx ctx);
-// ws: tree_simt_workspace(d) bytes.
-size_t tree_simt_workspace(int d);
-int tree_simt_ctas();
-cudaError_t launch_tree_simt(DType dt, KvFormat f, const void* q, const KvPages& pages,
-                             const uint64_t* masks, void* o, const int32_t* ctx_len, int max_ctx,
-                             int B, int H, int Hkv, int T, int d, float scale, void* ws,
-                             cudaStream_t st, DevCtx ctx);
+// New tokens over the paged cache: fp32 on the CUDA cores, bf16 on the tensor cores.  rows = H / Hkv * T
+// query rows per KV head; ws: tree_simt_workspace(rows, d) or tree_tc_workspace(rows, d) bytes.
+size_t tree_simt_workspace(int rows, int d);
+cudaError_t launch_tree_simt(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
+                             const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
+                             float scale, void* ws, cudaStream_t st, DevCtx ctx);
+size_t tree_tc_workspace(int rows, int d);
+cudaError_t launch_tree_tc(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
+                           const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
+                           float scale, void* ws, cudaStream_t st, DevCtx ctx);
 // Adds up the partials that the attention kernel's CTAs left (launched as its programmatic
 // dependent: it waits for that kernel before it reads anything).
 cudaError_t launch_tree_join(DType dt, const tree::Partials& part, void* out, const tree::Shape& s,

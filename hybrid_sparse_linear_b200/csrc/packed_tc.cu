@@ -405,7 +405,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t pk[16];
-                        exp32<false>(sr + 32 * c, sl2, nb, 0, acc, pk);
+                        exp32<false, false>(sr + 32 * c, sl2, nb, 0u, nullptr, acc, pk);
                         tmem_st16(colS + 16 * c, pk);
                     }
                 } else {
@@ -418,14 +418,14 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     tmem_ld_wait();
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        if (32 * c < keys) mx = max2n(mx, max32_masked(sr + 32 * c, lim - 32 * c));
+                        if (32 * c < keys) mx = max2n(mx, max32_masked(sr + 32 * c, bits_to(lim - 32 * c)));
                     alpha = st.raise(mx * sl2);
                     const float nb = st.shift();
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         if (32 * c < keys) {
                             uint32_t pk[16];
-                            exp32<true>(sr + 32 * c, sl2, nb, lim - 32 * c, acc, pk);
+                            exp32<true, false>(sr + 32 * c, sl2, nb, bits_to(lim - 32 * c), nullptr, acc, pk);
                             tmem_st16(colS + 16 * c, pk);
                         }
                 }

@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t (&chunk(uint32_t (&a)[kKeys], int c))[32] {
     return *reinterpret_cast<uint32_t(*)[32]>(a + 32 * c);
 }
 
-// Maximum of 32 logits; of those at positions 0 .. lim (-inf when lim < 0).
+// Maximum of 32 logits; of those whose bit in seen is set (-inf when none is).
 __device__ __forceinline__ float max32(const uint32_t* s) {
     float m[2];
 #pragma unroll
@@ -79,18 +79,24 @@ __device__ __forceinline__ float max32(const uint32_t* s) {
     }
     return max2n(m[0], m[1]);
 }
-__device__ __forceinline__ float max32_masked(const uint32_t* s, int lim) {
+__device__ __forceinline__ float max32_masked(const uint32_t* s, uint32_t seen) {
     float m[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int k = 0; k < 32; ++k) m[k & 1] = max2n(m[k & 1], k <= lim ? __uint_as_float(s[k]) : -INFINITY);
+    for (int k = 0; k < 32; ++k)
+        m[k & 1] = max2n(m[k & 1], ((seen >> k) & 1u) ? __uint_as_float(s[k]) : -INFINITY);
     return max2n(m[0], m[1]);
+}
+// Bits 0 .. lim of 32.
+__device__ __forceinline__ uint32_t bits_to(int lim) {
+    return lim >= 31 ? 0xffffffffu : lim < 0 ? 0u : (2u << lim) - 1u;
 }
 
 // p = 2^(s * sl2 + nb) for 32 logits as 16 bf16 pairs; sums of the unrounded p in acc[0..3].
-// kMasked: positions past lim give exact zeros.
-template <bool kMasked>
-__device__ __forceinline__ void exp32(const uint32_t* s, float sl2, float nb, int lim, float (&acc)[4],
-                                      uint32_t (&pk)[16]) {
+// kMasked: positions whose bit in seen is clear give exact zeros.  kScaled: the pairs hold p times
+// the key's entry of vs (the scale of its row of V), rounded once.
+template <bool kMasked, bool kScaled>
+__device__ __forceinline__ void exp32(const uint32_t* s, float sl2, float nb, uint32_t seen, const float* vs,
+                                      float (&acc)[4], uint32_t (&pk)[16]) {
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
         const int k = 2 * q;
@@ -105,11 +111,20 @@ __device__ __forceinline__ void exp32(const uint32_t* s, float sl2, float nb, in
             p1 = ex2(y1);
         }
         if (kMasked) {
-            p0 = k <= lim ? p0 : 0.f;
-            p1 = k + 1 <= lim ? p1 : 0.f;
+            p0 = ((seen >> k) & 1u) ? p0 : 0.f;
+            p1 = ((seen >> (k + 1)) & 1u) ? p1 : 0.f;
         }
         if (q & 1) add2(acc[2], acc[3], p0, p1);
         else add2(acc[0], acc[1], p0, p1);
+        if (kScaled) {
+            const float2 v = *reinterpret_cast<const float2*>(vs + k);
+            p0 *= v.x;
+            p1 *= v.y;
+            if (kMasked) {  // a hidden row's scale may be anything
+                p0 = ((seen >> k) & 1u) ? p0 : 0.f;
+                p1 = ((seen >> (k + 1)) & 1u) ? p1 : 0.f;
+            }
+        }
         pk[q] = pack_bf16x2(p0, p1);
     }
 }

@@ -1,0 +1,736 @@
+// Attention of new (drafted) tokens over a paged key/value cache on the 5th-generation tensor cores:
+// bf16 queries; the cache in bf16 or as 8-bit codes with one scale per row.
+//
+// The G * T query rows of a KV head are its M: rows (head g, token t) are contiguous in q.  Above 128
+// rows an item takes 256 (two tiles A and B that share every K and V tile); up to 128 rows there is
+// one tile of rows, and A takes the even, B the odd key tiles of the CTA's run, each with its own
+// accumulator, joined at the end: either way two chains S -> softmax -> PV run against each other.
+// Work is divided by key tiles of 128 (tree_plan.cuh), so a single sequence uses every SM.
+//
+// Bound: HBM for few rows (a key and value row are read once per 256 query rows: 4 G T d flops
+// against 4 d bytes, 2 (d + 4) in 8 bits), the tensor pipe from about T = 16 at G = 16.
+//
+// 8-bit caches.  Codes are at most 8 bits wide, so each is a bf16 number exactly; a warpgroup turns
+// the raw bytes of a tile into bf16 tiles in shared memory and the matrix products run as for bf16.
+// The scales never touch the tiles: a key's scale multiplies its column of S, a value's scale its
+// column of P (before P's one rounding to bf16, after the row sum), both in 32 bits.
+//
+// Hidden positions (drafts a row does not attend to, slots behind the last token, pages the table
+// does not hold) are left out by selection.  In a bf16 cache a hidden row of V could still turn a
+// probability of zero into NaN, so one warp looks through the V tiles that hold such rows: rows
+// nobody sees become zero; an infinity or NaN in a draft's row becomes zero and is noted per column,
+// and the epilogue gives it to the rows that attend to that draft.
+//
+// Roles: warps 0-3 softmax and epilogue of tile A, 4-7 of B; 8 walks the items and loads (TMA for
+// bf16 tiles, bulk copies for codes and scales); 9 and 10 issue the MMAs of A and B; 11 looks through
+// V (bf16); 12-15 (8-bit caches only) convert.  Every wait is bounded.
+#include <type_traits>
+
+#include "kv_format.cuh"
+#include "softmax_tile.cuh"
+#include "tmap.cuh"
+#include "tree_plan.cuh"
+
+namespace sala {
+namespace {
+
+using namespace ptx;
+using namespace smx;
+
+constexpr int kConvThreads = 128;
+
+template <int D, KvFormat F, bool kWide>
+struct Layout {
+    static constexpr bool kCodes = F != KvFormat::Same;
+    static constexpr int kThreads = kCodes ? 512 : 384;
+    static constexpr int kRegsSoft = kCodes ? 200 : 216, kRegsRest = kCodes ? 56 : 72;
+    static constexpr int kRows = kWide ? 256 : 128;          // query rows per item
+    static constexpr int kBox = 128 * 128;                   // [128 rows x 64 columns] bf16, swizzled
+    static constexpr int kTile = (D / 64) * kBox;            // one Q, K or V tile
+    static constexpr int kRaw = kKeys * D;                   // the codes of one
+    // K and V tiles: one ring that both tiles of rows use, or one for each.
+    static constexpr int kRing = (kWide ? (kCodes ? 3 : 5) : (kCodes ? 2 : 3)) * (128 / D);
+    static constexpr int kSlots = kWide ? kRing : 2 * kRing;
+    static constexpr int kRawSlots = kCodes ? 3 * (128 / D) : 0;
+    // The tiles first (each 1024-byte aligned), then the small parts.
+    static constexpr int kOffRing = (kWide ? 2 : 1) * kTile;
+    static constexpr int kOffRaw = kOffRing + kSlots * kTile;
+    static constexpr int kOffRawScale = kOffRaw + kRawSlots * kRaw;
+    static constexpr int kOffScale = kOffRawScale + kRawSlots * kKeys * 4;
+    static constexpr int kOffNotes = kOffScale + (kCodes ? kSlots * kKeys * 4 : 0);
+    static constexpr int kNoteBytes = kCodes ? 0 : 2 * D * 8;    // sign x column, a bit per draft
+    static constexpr int kOffBars = kOffNotes + kNoteBytes;
+};
+
+// An item's part in this CTA's run.
+struct Item {
+    int b, g, rt, ctx;
+    int tile, n;      // key tiles [tile, tile + n) (n 0: no more)
+    int first, whole;  // the run's first item; the run covers the item whole
+};
+// A V tile to look through.
+struct Look {
+    int slot;     // where it is
+    int k0, ctx;  // its first key; the sequence's context length
+    int pages;    // bit 0, 1: the half's page holds keys
+    int it, last;  // the item, and whether this is its last tile with drafts
+};
+
+template <class L>
+struct Bars {
+    uint64_t full[L::kSlots], empty[L::kSlots];
+    uint64_t raw_full[L::kRawSlots + 1], raw_empty[L::kRawSlots + 1];
+    uint64_t q_full[2], q_empty;
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t v_landed[2], look_free[2];  // alternating over the looks
+    uint64_t v_seen[2];                  // per item parity: its drafts' V is looked through
+    uint64_t b_done, merged;             // tile B's accumulator is complete; tile A has read it
+    uint64_t item_full[2], item_empty[2];
+    uint64_t fin[2];
+    Item item[2];
+    Look look[2];
+    int pages[L::kSlots];                // as Look::pages, per K tile
+    int raw_pages[L::kRawSlots + 1];
+    int noted_it;                        // the item that the notes belong to
+    uint32_t tmem_base;
+    int abort;
+};
+
+// bf16 pairs of four codes.
+template <KvFormat F>
+__device__ __forceinline__ uint2 codes_to_bf16(uint32_t c) {
+    if constexpr (F == KvFormat::Int8) {
+        // A byte u in 16 bits: 128 + (u & 127) and 128 or 256 (bit 7 is the last exponent bit of
+        // 0x4300 = 128) are bf16 numbers, and their difference is the signed byte, exactly.
+        auto two = [](uint32_t u) {
+            const uint32_t a = (u & 0x007f007fu) | 0x43004300u, b = (u & 0x00800080u) | 0x43004300u;
+            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&b));
+            return *reinterpret_cast<const uint32_t*>(&d);
+        };
+        return make_uint2(two(__byte_perm(c, 0u, 0x4140)), two(__byte_perm(c, 0u, 0x4342)));
+    } else {
+        // s eeee mmm moved to bf16's places is the value times 2^-120 (the biases differ by 120, and
+        // e4m3's subnormals become bf16's); the product with 2^120 is exact.
+        const uint32_t k = 0x7b807b80u;  // 2^120
+        auto two = [&](uint32_t h) {     // the byte in the high half of each 16 bits
+            const uint32_t a = ((h >> 4) & 0x07f007f0u) | (h & 0x80008000u);
+            const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&k));
+            return *reinterpret_cast<const uint32_t*>(&d);
+        };
+        return make_uint2(two(__byte_perm(c, 0u, 0x1404)), two(__byte_perm(c, 0u, 0x3424)));
+    }
+}
+
+template <int D, KvFormat F, bool kWide>
+__global__ void __launch_bounds__(Layout<D, F, kWide>::kThreads, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, KvPages pages, const uint64_t* __restrict__ masks,
+               __nv_bfloat16* __restrict__ out, tree::Shape s, tree::Partials part, float sl2, DevCtx ctx) {
+    using L = Layout<D, F, kWide>;
+    static_assert(L::kOffBars + sizeof(Bars<L>) <= 227 * 1024, "shared memory");
+    constexpr bool kCodes = L::kCodes;
+    constexpr uint32_t kRing = L::kRing, kSlots = L::kSlots, kRawSlots = kCodes ? L::kRawSlots : 1;
+    constexpr uint32_t kColO = 0, kColS = 256;
+    extern __shared__ __align__(1024) uint8_t sm[];  // all of the block's shared memory
+    Bars<L>& bars = *reinterpret_cast<Bars<L>*>(sm + L::kOffBars);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* abort = &bars.abort;
+    unsigned long long* notes = reinterpret_cast<unsigned long long*>(sm + L::kOffNotes);
+
+    cudaTriggerProgrammaticLaunchCompletion();  // the join may be set up; it waits for this grid's end
+    if (warp == 9) {
+        tmem_alloc(&bars.tmem_base, 512);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (uint32_t i = 0; i < kSlots; ++i) {
+            mbar_init(&bars.full[i], kCodes ? kConvThreads / 32 : 1);
+            mbar_init(&bars.empty[i], kWide ? 8 : 4);  // the softmax warps of the tiles that use it
+        }
+        for (uint32_t i = 0; i < kRawSlots; ++i) {
+            mbar_init(&bars.raw_full[i], 1);
+            mbar_init(&bars.raw_empty[i], kConvThreads / 32);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&bars.q_full[x], 1);
+            mbar_init(&bars.s_full[x], 1);
+            mbar_init(&bars.p_full[x], 4);
+            mbar_init(&bars.o_full[x], 1);
+            mbar_init(&bars.v_landed[x], 1);
+            mbar_init(&bars.look_free[x], 1);
+            mbar_init(&bars.v_seen[x], 1);
+            mbar_init(&bars.item_full[x], 1);
+            mbar_init(&bars.item_empty[x], 10 + (kCodes ? 4 : 0));  // softmax, issuers, converters
+            mbar_init(&bars.fin[x], 1);
+        }
+        mbar_init(&bars.q_empty, 2);
+        mbar_init(&bars.b_done, 4);
+        mbar_init(&bars.merged, 4);
+        bars.noted_it = -1;
+        bars.abort = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base;
+
+    // Entry e of a ring (K and V of its key tiles in turn) lives in its slot e % kRing, as that slot's
+    // use number e / kRing.  Who waits for an entry has waited for all before it in that ring, so no
+    // parity wait runs two uses ahead, and none falls two behind: an entry is not overwritten before
+    // every tile that uses it has handed it back.
+    auto ring_of = [](int x) { return kWide ? 0u : (uint32_t)x; };
+    auto slot_of = [&](int x, uint32_t e) { return ring_of(x) * kRing + e % kRing; };
+    auto use_of = [](uint32_t e) { return (e / kRing) & 1u; };
+    auto slot_ptr = [&](uint32_t slot) { return sm + L::kOffRing + slot * L::kTile; };
+    auto raw_of = [](uint32_t e) { return e % kRawSlots; };
+    auto raw_use = [](uint32_t e) { return (e / kRawSlots) & 1u; };
+    auto take_item = [&](int it, Item& m) -> bool {
+        if (!wait_warp(&bars.item_full[it & 1], (it >> 1) & 1, ctx, abort)) return false;
+        m = bars.item[it & 1];
+        return m.n > 0;
+    };
+    auto leave_item = [&](int it) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.item_empty[it & 1]);
+    };
+    // Key tiles of tile x of an item with n of them: all, or every other one.
+    auto my_tiles = [](int n, int x) { return kWide ? n : (n + 1 - x) / 2; };
+    auto nth_tile = [](int k, int x) { return kWide ? k : 2 * k + x; };
+
+    if (warp >= 8) {
+        set_regs_down<L::kRegsRest>();
+        if (warp == 8) {
+            // ------------------------------------------------------------ items and loads
+            bool bad = false;
+            const long long w = tree::total_tiles(s, lane, &bad);
+            if (bad && blockIdx.x == 0) flag(ctx, kStatusBounds);
+            const long long x0 = tree::run_start(w, blockIdx.x, gridDim.x);
+            tree::Cursor c = tree::find_tile(s, x0, tree::run_start(w, blockIdx.x + 1, gridDim.x) - x0, lane);
+            uint32_t rc[2] = {0, 0}, rr = 0, kq = 0, looks = 0;  // entries, raw tiles, Q tiles, looks
+            uint32_t via = 0;  // slots whose last load went to v_landed
+            bool ok = true;
+            for (int it = 0; ok; ++it) {
+                const int n = tree::run_tiles(c);
+                if (it >= 2 && !wait_warp(&bars.item_empty[it & 1], ((it - 2) >> 1) & 1, ctx, abort)) break;
+                if (lane == 0) {
+                    bars.item[it & 1] = Item{c.b, c.g, c.rt, c.ctx, c.tile, n, it == 0, n == c.n_tiles};
+                    mbar_arrive(&bars.item_full[it & 1]);
+                }
+                if (n == 0) break;
+                if (kq >= 1 && !wait_warp(&bars.q_empty, (kq - 1) & 1, ctx, abort)) break;
+                if (lane == 0) {
+                    const int y = (c.b * s.Hkv + c.g) * s.rows + c.rt * L::kRows;
+                    for (int x = 0; x < (kWide ? 2 : 1); ++x) {
+                        mbar_arrive_expect_tx(&bars.q_full[x], L::kTile);
+                        for (int h = 0; h < D / 64; ++h)
+                            tma_load_2d(sm + x * L::kTile + h * L::kBox, &tmQ, &bars.q_full[x], 64 * h, y + 128 * x);
+                    }
+                }
+                ++kq;
+                const int keys = c.ctx + s.T;
+                int ids = -1;
+                for (int i = 0; ok && i < n; ++i) {
+                    const int t = c.tile + i;
+                    if ((i & 15) == 0) ids = page_of(pages, c.b, 2 * t + lane);  // of 16 key tiles
+                    int id[2];
+                    int have = 0;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        id[h] = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + h);
+                        if (t * kKeys + h * kPage < keys) {
+                            if (id[h] >= 0) have |= 1 << h;
+                            else if (lane == 0) flag(ctx, kStatusBounds);  // left out
+                        }
+                    }
+                    const bool drafts = (t + 1) * kKeys > c.ctx;  // keys that some row does not see
+                    for (int j = 0; ok && j < 2; ++j) {  // K, V
+                        const int row[2] = {(id[0] * s.Hkv + c.g) * kPage, (id[1] * s.Hkv + c.g) * kPage};
+                        if constexpr (kCodes) {
+                            const uint32_t q = raw_of(rr);
+                            if (rr >= kRawSlots && !(ok = wait_warp(&bars.raw_empty[q], raw_use(rr - kRawSlots), ctx, abort)))
+                                break;
+                            ++rr;
+                            if (lane == 0) {
+                                bars.raw_pages[q] = have;
+                                mbar_arrive_expect_tx(&bars.raw_full[q], __popc(have) * (kPage * D + kPage * 4));
+                                const uint8_t* codes = static_cast<const uint8_t*>(j ? pages.v : pages.k);
+                                const float* scales = j ? pages.v_scale : pages.k_scale;
+                                for (int h = 0; h < 2; ++h)
+                                    if ((have >> h) & 1) {
+                                        bulk_load_g2s(sm + L::kOffRaw + q * L::kRaw + h * kPage * D,
+                                                      codes + (int64_t)row[h] * D, kPage * D, &bars.raw_full[q]);
+                                        bulk_load_g2s(sm + L::kOffRawScale + (q * kKeys + h * kPage) * 4,
+                                                      scales + row[h], kPage * 4, &bars.raw_full[q]);
+                                    }
+                            }
+                        } else {
+                            const bool odd = !kWide && (i & 1);
+                            const uint32_t e = odd ? rc[1] : rc[0], q = slot_of(odd, e);
+                            if (e >= kRing && !(ok = wait_warp(&bars.empty[q], use_of(e - kRing), ctx, abort)))
+                                break;
+                            const bool look = j == 1 && (drafts || have != 3);
+                            if (look && looks >= 2 &&
+                                !(ok = wait_warp(&bars.look_free[looks & 1], ((looks - 2) >> 1) & 1, ctx, abort)))
+                                break;
+                            if (lane == 0) {
+                                uint64_t* fb = look ? &bars.v_landed[looks & 1] : &bars.full[q];
+                                if (j == 0) bars.pages[q] = have;
+                                if (look) bars.look[looks & 1] = Look{(int)q, t * kKeys, c.ctx, have, it, drafts && i == n - 1};
+                                mbar_arrive_expect_tx(fb, __popc(have) * (L::kTile / 2));
+                                for (int h = 0; h < 2; ++h)
+                                    if ((have >> h) & 1)
+                                        for (int p = 0; p < D / 64; ++p)
+                                            tma_load_2d(slot_ptr(q) + p * L::kBox + h * (L::kBox / 2),
+                                                        j ? &tmV : &tmK, fb, 64 * p, row[h]);
+                            }
+                            via = (via & ~(1u << q)) | ((look ? 1u : 0u) << q);
+                            looks += look ? 1 : 0;
+                            if (odd) ++rc[1];
+                            else ++rc[0];
+                        }
+                    }
+                }
+                tree::next_item(s, c);
+            }
+            if constexpr (!kCodes) {  // no more looks: an entry that says so
+                if (ok && looks >= 2) ok = wait_warp(&bars.look_free[looks & 1], ((looks - 2) >> 1) & 1, ctx, abort);
+                if (ok && lane == 0) {
+                    bars.look[looks & 1].it = -1;
+                    mbar_arrive(&bars.v_landed[looks & 1]);
+                }
+            }
+            if (lane == 0) {  // drain: every copy this warp started has landed before the block exits
+                if (kq > 0)
+                    for (int x = 0; x < (kWide ? 2 : 1); ++x) (void)mbar_wait(&bars.q_full[x], (kq - 1) & 1, ctx);
+                if constexpr (kCodes) {
+                    for (uint32_t e = rr > kRawSlots ? rr - kRawSlots : 0; e < rr; ++e)
+                        (void)mbar_wait(&bars.raw_full[raw_of(e)], raw_use(e), ctx);
+                } else {
+                    for (uint32_t l = looks > 2 ? looks - 2 : 0; l < looks; ++l)
+                        // (a barrier that went on to the closing entry has this use behind it)
+                        if (!ok || l != looks - 2) (void)mbar_wait(&bars.v_landed[l & 1], (l >> 1) & 1, ctx);
+                    for (int x = 0; x < (kWide ? 1 : 2); ++x)
+                        for (uint32_t e = rc[x] > kRing ? rc[x] - kRing : 0; e < rc[x]; ++e)
+                            if (!((via >> slot_of(x, e)) & 1u))
+                                (void)mbar_wait(&bars.full[slot_of(x, e)], use_of(e), ctx);
+                }
+            }
+        } else if (warp < 11) {
+            // ------------------------------------------------------------ MMA issuers
+            // As in the packed kernel: S of the tile's next key tile right behind PV of this one.
+            const int x = warp - 9;
+            auto wait_w = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, ctx, abort); };
+            const uint32_t dO = tmem + kColO + x * 128, dS = tmem + kColS + x * 128;
+            const uint64_t dhi = (uint64_t)sdesc_sw128_hi(1024) << 32;
+            const uint64_t q_d = dhi | sdesc_sw128_lo(smem_u32(sm + (kWide ? x : 0) * L::kTile), 16);
+            const uint64_t k_d0 = dhi | sdesc_sw128_lo(smem_u32(sm + L::kOffRing), 16);
+            const uint64_t v_d0 = dhi | sdesc_sw128_lo(smem_u32(sm + L::kOffRing), L::kBox);
+            constexpr uint32_t idS = idesc_bf16_f32(128, kKeys, false, false);
+            constexpr uint32_t idPV = idesc_bf16_f32(128, D, false, true);
+            uint32_t rc = 0, np = 0;
+            bool ok = true;
+            Item m;
+            for (int it = 0; ok && take_item(it, m); ++it) {
+                const int nx = my_tiles(m.n, x);
+                auto issue_s = [&](int k) -> bool {
+                    const uint32_t e = rc + 2 * k, q = slot_of(x, e);
+                    if (!wait_w(&bars.full[q], use_of(e))) return false;
+                    tc_fence_after();
+                    const uint64_t k_d = k_d0 + q * (L::kTile >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * L::kBox + (ks & 3) * 32) >> 4;
+                        mma_ss_elect(dS, q_d + off, k_d + off, idS, ks > 0 ? 1u : 0u);
+                    }
+                    mma_commit_elect(&bars.s_full[x]);
+                    return true;
+                };
+                ok = wait_w(&bars.q_full[kWide ? x : 0], it & 1) && (nx == 0 || issue_s(0));
+                for (int k = 0; ok && k < nx; ++k) {
+                    const uint32_t e = rc + 2 * k + 1, q = slot_of(x, e);
+                    ok = wait_w(&bars.p_full[x], np++ & 1) && wait_w(&bars.full[q], use_of(e));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t v_d = v_d0 + q * (L::kTile >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                        mma_ts_elect(dO, dS + ks * 8, v_d + ((ks * 16 * 128) >> 4), idPV, (k > 0 || ks > 0) ? 1u : 0u);
+                    if (k + 1 < nx) ok = issue_s(k + 1);
+                }
+                rc += 2 * nx;
+                if (ok) mma_commit_elect(&bars.q_empty);  // every S that reads this item's Q is done
+                if (ok && nx > 0) mma_commit_elect(&bars.o_full[x]);
+                leave_item(it);
+            }
+            mma_commit_elect(&bars.fin[x]);
+            (void)mbar_wait(&bars.fin[x], 0, ctx);
+            __syncwarp();
+        } else if (warp == 11) {
+            // ------------------------------------------------------------ V rows not every row sees
+            if constexpr (!kCodes) {
+                for (uint32_t l = 0;; ++l) {
+                    if (!wait_warp(&bars.v_landed[l & 1], (l >> 1) & 1, ctx, abort)) break;
+                    const Look v = bars.look[l & 1];
+                    if (v.it < 0) break;
+                    constexpr int kC = D / 8;  // 16-byte pieces per row
+                    uint8_t* tile = slot_ptr(v.slot);
+                    const int keys = v.ctx + s.T;
+                    for (int c0 = 0; c0 < kKeys * kC; c0 += 32) {
+                        const int r = (c0 + lane) / kC, c = (c0 + lane) % kC, j = v.k0 + r - v.ctx;
+                        uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * L::kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                        bool bad = false;
+                        if (v.k0 + r >= keys || !((v.pages >> (r >> 6)) & 1)) *p = make_uint4(0u, 0u, 0u, 0u);
+                        else if (j >= 0) bad = any_nonfinite8(*p);
+                        unsigned todo = __ballot_sync(0xffffffffu, bad);
+                        if (todo == 0u) continue;
+                        if (*reinterpret_cast<volatile int*>(&bars.noted_it) != v.it) {
+                            // The notes may still be read for the item before.
+                            if (v.it >= 1) (void)wait_warp(&bars.item_empty[(v.it - 1) & 1], ((v.it - 1) >> 1) & 1, ctx, abort);
+                            for (int e = lane; e < 2 * D; e += 32) notes[e] = 0ull;
+                            __syncwarp();
+                            if (lane == 0) *reinterpret_cast<volatile int*>(&bars.noted_it) = v.it;
+                            __syncwarp();
+                        }
+                        for (; todo; todo &= todo - 1) {  // one lane after another: they share columns
+                            if (lane == __ffs((int)todo) - 1) {
+                                uint16_t* e = reinterpret_cast<uint16_t*>(p);
+                                for (int q = 0; q < 8; ++q) {
+                                    if ((e[q] & 0x7f80u) != 0x7f80u) continue;
+                                    const bool nan = (e[q] & 0x7fu) != 0u, neg = (e[q] & 0x8000u) != 0u;
+                                    if (nan || !neg) notes[c * 8 + q] |= 1ull << j;
+                                    if (nan || neg) notes[D + c * 8 + q] |= 1ull << j;
+                                    e[q] = 0;
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    fence_proxy_async_smem();  // the MMA reads what was just written
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bars.full[v.slot]);
+                        if (v.last) mbar_arrive(&bars.v_seen[v.it & 1]);
+                        mbar_arrive(&bars.look_free[l & 1]);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else {
+            // ------------------------------------------------------------ codes to bf16 tiles
+            if constexpr (kCodes) {
+                const int ct = tid - 12 * 32;
+                uint32_t rc[2] = {0, 0}, rr = 0;
+                bool ok = true;
+                Item m;
+                for (int it = 0; ok && take_item(it, m); ++it) {
+                    for (int i = 0; ok && i < 2 * m.n; ++i, ++rr) {
+                        const bool odd = !kWide && ((i >> 1) & 1);
+                        const uint32_t e2 = odd ? rc[1]++ : rc[0]++, q = slot_of(odd, e2);
+                        ok = wait_warp(&bars.raw_full[raw_of(rr)], raw_use(rr), ctx, abort);
+                        if (ok && e2 >= kRing) ok = wait_warp(&bars.empty[q], use_of(e2 - kRing), ctx, abort);
+                        if (!ok) break;
+                        const uint8_t* raw = sm + L::kOffRaw + raw_of(rr) * L::kRaw;
+                        uint8_t* tile = slot_ptr(q);
+                        // A lane takes 16 codes, four lanes 64 columns of a row, neighbouring rows the
+                        // other 64: eight lanes then read and (through the swizzle) write all 32 banks.
+                        constexpr int kC = D / 16;
+#pragma unroll 4
+                        for (int e = ct; e < kKeys * kC; e += kConvThreads) {
+                            const int r = (e >> 2) % kKeys, c = e & 3;
+                            const int box = D == 64 ? 0 : (r + e / (kKeys * 4)) & 1;
+                            const uint4 u = *reinterpret_cast<const uint4*>(raw + r * D + box * 64 + c * 16);
+                            uint8_t* row = tile + box * L::kBox + r * 128;
+                            const uint2 a0 = codes_to_bf16<F>(u.x), a1 = codes_to_bf16<F>(u.y);
+                            const uint2 a2 = codes_to_bf16<F>(u.z), a3 = codes_to_bf16<F>(u.w);
+                            *reinterpret_cast<uint4*>(row + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+                            *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
+                        }
+                        reinterpret_cast<float*>(sm + L::kOffScale)[q * kKeys + ct] =
+                            reinterpret_cast<const float*>(sm + L::kOffRawScale)[raw_of(rr) * kKeys + ct];
+                        if (ct == 0) bars.pages[q] = bars.raw_pages[raw_of(rr)];
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&bars.full[q]);
+                            mbar_arrive(&bars.raw_empty[raw_of(rr)]);
+                        }
+                    }
+                    leave_item(it);
+                }
+            }
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax + epilogue
+        set_regs_up<L::kRegsSoft>();
+        const int x = warp >> 2;
+        const int r = tid & 127;
+        const uint32_t lane_base = tmem_lane_base(warp);
+        const uint32_t colO = tmem + lane_base + kColO + x * 128;
+        const uint32_t colS = tmem + lane_base + kColS + x * 128;
+        uint32_t rc = 0, rb = 0;  // entries of the tile's ring; of tile B's
+        uint32_t ns = 0, no = 0, n_two = 0, nseen[2] = {0, 0};
+        bool ok = true;
+        auto give = [&](uint32_t slot) {  // this warp is done with what is there
+            if (lane == 0) mbar_arrive(&bars.empty[slot]);
+        };
+        Item m;
+        for (int it = 0; ok && take_item(it, m); ++it) {
+            const int nx = my_tiles(m.n, x);
+            const int row = m.rt * L::kRows + (kWide ? r + 128 * x : r);  // of the group
+            const bool real = row < s.rows;
+            const uint64_t bits = real ? tree::draft_bits(masks, m.b, row % s.T, s.T) : 0ull;
+            const bool any_real = __any_sync(0xffffffffu, real);  // else the warp only passes stages on
+            RowState st;
+            for (int k = 0; k < nx; ++k, ++ns) {
+                const int i = nth_tile(k, x), k0 = (m.tile + i) * kKeys;
+                const uint32_t e = rc + 2 * k, qk = slot_of(x, e), qv = slot_of(x, e + 1);
+                ok = wait_warp(&bars.s_full[x], ns & 1, ctx, abort) &&
+                     wait_warp(&bars.full[qk], use_of(e), ctx, abort);  // (done: for its pages, scales)
+                if (!ok) break;
+                tc_fence_after();
+                // PV of the tile before is done (S was committed behind it).  Its V goes back before this
+                // tile's is waited for below: they may share the slot.
+                if (k > 0) give(slot_of(x, e - 1));
+                float alpha = 1.f;
+                if (any_real) {
+                    uint32_t sr[kKeys];
+                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld32(colS + 32 * c, chunk(sr, c));
+                    const int have = bars.pages[qk];
+                    tmem_ld_wait();
+                    if constexpr (kCodes) {
+                        const float* ks = reinterpret_cast<const float*>(sm + L::kOffScale) + qk * kKeys;
+#pragma unroll
+                        for (int c = 0; c < kKeys; c += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(ks + c);
+                            sr[c] = __float_as_uint(__uint_as_float(sr[c]) * f.x);
+                            sr[c + 1] = __float_as_uint(__uint_as_float(sr[c + 1]) * f.y);
+                            sr[c + 2] = __float_as_uint(__uint_as_float(sr[c + 2]) * f.z);
+                            sr[c + 3] = __float_as_uint(__uint_as_float(sr[c + 3]) * f.w);
+                        }
+                    }
+                    const float* vs = reinterpret_cast<const float*>(sm + L::kOffScale) + qv * kKeys;
+                    if (k0 + kKeys <= m.ctx && have == 3) {
+                        const float mx = max2n(max2n(max32(sr), max32(sr + 32)), max2n(max32(sr + 64), max32(sr + 96)));
+                        alpha = st.raise(mx * sl2);
+                        const float nb = st.shift();
+                        // The scales of V's rows are there once V is (the softmax of codes waits for it).
+                        if (kCodes) ok = wait_warp(&bars.full[qv], use_of(e + 1), ctx, abort);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t pk[16];
+                            exp32<false, kCodes>(sr + 32 * c, sl2, nb, 0u, vs + 32 * c, acc, pk);
+                            tmem_st16(colS + 16 * c, pk);
+                        }
+                    } else {
+                        uint32_t seen[4];
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int d0 = k0 + 32 * c - m.ctx;  // draft number of the chunk's first key
+                            const uint32_t drafts = d0 >= 64 ? 0u : d0 >= 0 ? (uint32_t)(bits >> d0)
+                                                  : d0 > -32 ? (uint32_t)(bits << -d0) : 0u;
+                            seen[c] = ((have >> (c >> 1)) & 1) ? (bits_to(-d0 - 1) | drafts) : 0u;
+                            mx = max2n(mx, max32_masked(sr + 32 * c, seen[c]));
+                        }
+                        alpha = st.raise(mx * sl2);
+                        const float nb = st.shift();
+                        if (kCodes) ok = wait_warp(&bars.full[qv], use_of(e + 1), ctx, abort);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t pk[16];
+                            exp32<true, kCodes>(sr + 32 * c, sl2, nb, seen[c], vs + 32 * c, acc, pk);
+                            tmem_st16(colS + 16 * c, pk);
+                        }
+                    }
+                    st.l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+                }
+                __syncwarp();
+                give(qk);  // S is done with K, and this warp with its scales
+                if (!ok) break;
+                // Tile A reads tile B's accumulator at an item's end: B writes P, which lets the issuer
+                // start on it, only after that.
+                if (!kWide && x == 1 && k == 0 && no > 0) ok = wait_warp(&bars.merged, (no - 1) & 1, ctx, abort);
+                if (!ok) break;
+                if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) scale_row<D>(colO, alpha);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.p_full[x]);
+            }
+            if (!ok) break;
+            // The drafts' V of this item is looked through (its notes can be read).
+            bool noted = false;
+            if constexpr (!kCodes) {
+                if ((m.tile + m.n) * kKeys > m.ctx) {
+                    ok = wait_warp(&bars.v_seen[it & 1], nseen[it & 1]++ & 1, ctx, abort);
+                    if (!ok) break;
+                    noted = *reinterpret_cast<volatile int*>(&bars.noted_it) == it;
+                }
+            }
+            // Tile B's maxima and sums go to tile A through B's last V tile, which A hands back.
+            float2* merge = nullptr;
+            if (nx > 0) {
+                ok = wait_warp(&bars.o_full[x], no & 1, ctx, abort);
+                if (!ok) break;
+                tc_fence_after();
+                ++no;
+                rc += 2 * nx;
+                if (kWide || x == 0) give(slot_of(x, rc - 1));
+            }
+            if (!kWide) {
+                rb += 2 * my_tiles(m.n, 1);
+                merge = reinterpret_cast<float2*>(slot_ptr(slot_of(1, rb - 1)));
+                if (x == 1) {
+                    if (nx > 0) {
+                        merge[r] = make_float2(st.m, st.l);
+                        fence_proxy_async_smem();  // the next tile's copy comes behind it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars.b_done);
+                    }
+                    leave_item(it);
+                    continue;
+                }
+            }
+            const bool two = !kWide && m.n > 1;
+            float top = st.m, l = st.l, w_a = 1.f, w_b = 0.f;
+            if (two) {
+                ok = wait_warp(&bars.b_done, n_two++ & 1, ctx, abort);
+                if (!ok) break;
+                tc_fence_after();
+                const float2 o = merge[r];
+                top = fmaxf(st.m, o.x);
+                w_a = st.m == -INFINITY ? 0.f : ex2(st.m - top);
+                w_b = o.x == -INFINITY ? 0.f : ex2(o.x - top);
+                l = st.l * w_a + o.y * w_b;
+                __syncwarp();
+                give(slot_of(1, rb - 1));
+            }
+            const float inv = !m.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const int64_t orow = ((int64_t)m.b * s.Hkv + m.g) * s.rows + row;
+            const int rt = kWide ? L::kRows : s.rows;  // rows a partial slot holds
+            const size_t slot = ((size_t)blockIdx.x * 2 + (m.first ? 0 : 1)) * rt + (kWide ? r + 128 * x : r);
+            if (real && !m.whole) part.ml[slot] = make_float2(top, l);
+            if (any_real) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(colO + c0, o);
+                    if (two) {
+                        uint32_t q[32];
+                        tmem_ld32(colO + 128 + c0, q);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * w_a + __uint_as_float(q[e]) * w_b);
+                    } else {
+                        tmem_ld_wait();
+                    }
+                    if (noted) {  // rows that attend to a draft with an infinity or a NaN in V get it back
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float y = __uint_as_float(o[e]);
+                            if (notes[c0 + e] & bits) y += INFINITY;
+                            if (notes[D + c0 + e] & bits) y -= INFINITY;
+                            o[e] = __float_as_uint(y);
+                        }
+                    }
+                    if (!real) continue;
+                    if (m.whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(out + orow * D + c0);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
+                                                   __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
+                            dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(part.o + slot * D + c0);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (two && lane == 0) mbar_arrive(&bars.merged);
+            leave_item(it);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, KvFormat F, bool kWide>
+cudaError_t tree_tc(const void* q, const KvPages& pages, const uint64_t* masks, void* o, tree::Shape s,
+                    void* ws, float scale, cudaStream_t st, DevCtx ctx) {
+    using L = Layout<D, F, kWide>;
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return cudaErrorNotSupported;
+    auto map = [&](CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
+        return make_tmap_bf16_2d(m, base, D, rows, D, 64, box_rows);
+    };
+    CUtensorMap tmQ, tmK{}, tmV{};
+    if (cudaError_t e = map(&tmQ, q, (uint64_t)s.B * s.Hkv * s.rows, 128); e != cudaSuccess) return e;
+    if (F == KvFormat::Same && pages.n_pages > 0) {
+        const uint64_t rows = (uint64_t)pages.n_pages * s.Hkv * kPage;
+        if (cudaError_t e = map(&tmK, pages.k, rows, kPage); e != cudaSuccess) return e;
+        if (cudaError_t e = map(&tmV, pages.v, rows, kPage); e != cudaSuccess) return e;
+    }
+    constexpr int bytes = L::kOffBars + (int)sizeof(Bars<L>);
+    if (cudaError_t e = ensure_smem<tree_tc_kernel<D, F, kWide>>(bytes); e != cudaSuccess) return e;
+    s.n_rt = kWide ? tree::row_tiles(s.rows, L::kRows) : 1;
+    s.kt = kKeys;
+    const int tiles = (s.max_ctx + s.T + kKeys - 1) / kKeys;
+    const long long most = (long long)s.B * s.Hkv * s.n_rt * tiles;
+    const int sms = device_sm_count();
+    const int n_cta = most < sms ? (int)most : sms;
+    const int rt = kWide ? L::kRows : s.rows;
+    const tree::Partials part = tree::partials_at(ws, n_cta, rt);
+    tree_tc_kernel<D, F, kWide><<<n_cta, L::kThreads, bytes, st>>>(
+        tmQ, tmK, tmV, pages, masks, static_cast<__nv_bfloat16*>(o), s, part,
+        scale * 1.4426950408889634f, ctx);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (tiles == 1) return cudaSuccess;  // no item is ever split
+    return launch_tree_join(DType::BF16, part, o, s, rt, D, n_cta, st);
+}
+
+}  // namespace
+
+size_t tree_tc_workspace(int rows, int d) {
+    return tree::partial_bytes(device_sm_count(), rows > 128 ? 256 : rows, d);
+}
+
+cudaError_t launch_tree_tc(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
+                           const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
+                           float scale, void* ws, cudaStream_t st, DevCtx ctx) {
+    const tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, H / Hkv * T, 0, 0};
+    auto go = [&](auto dd, auto ff) {
+        constexpr int D = decltype(dd)::value;
+        constexpr KvFormat F = decltype(ff)::value;
+        return s.rows > 128 ? tree_tc<D, F, true>(q, pages, masks, o, s, ws, scale, st, ctx)
+                            : tree_tc<D, F, false>(q, pages, masks, o, s, ws, scale, st, ctx);
+    };
+    auto with_format = [&](auto dd) {
+        if (f == KvFormat::Int8) return go(dd, std::integral_constant<KvFormat, KvFormat::Int8>{});
+        if (f == KvFormat::E4M3) return go(dd, std::integral_constant<KvFormat, KvFormat::E4M3>{});
+        return go(dd, std::integral_constant<KvFormat, KvFormat::Same>{});
+    };
+    return d == 64 ? with_format(std::integral_constant<int, 64>{})
+                   : with_format(std::integral_constant<int, 128>{});
+}
+
+}  // namespace sala
