@@ -58,8 +58,11 @@ __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float 
 template <KvFormat F>
 __device__ __forceinline__ float4 decode4(uint32_t c) {
     if constexpr (F == KvFormat::Int8) {
-        return make_float4((float)(int8_t)c, (float)(int8_t)(c >> 8), (float)(int8_t)(c >> 16),
-                           (float)(int8_t)(c >> 24));
+        // code + 128 in the low mantissa byte of 2^23; the difference is the code, exactly
+        const uint32_t u = c ^ 0x80808080u;
+        constexpr uint32_t k = 0x4b000000u;  // 2^23
+        auto f = [&](uint32_t sel) { return __uint_as_float(__byte_perm(u, k, sel)) - 8388736.f; };
+        return make_float4(f(0x7440), f(0x7441), f(0x7442), f(0x7443));
     } else {
         const __half2 lo(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3));
         const __half2 hi(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3));

@@ -508,53 +508,72 @@ def sparse_decode_paged(q, k_pages, v_pages, page_table, kbar, pos, max_pos, top
 _NO_SWITCH = contextlib.nullcontext()
 
 
-def _on(t, stream, *others):
-    """Context in which a call on t's device allocates and launches: the given stream (whose pool
-    then owns what the call allocates), else t's device's current stream.  Every tensor of the call
-    has to lie on that device."""
-    for x in others:
-        if x is not None and x.device != t.device:
-            raise ValueError(f"tensors on {t.device} and {x.device}")
+def _on(dev, stream):
+    """Context in which a call on a device allocates and launches: the given stream (whose pool then
+    owns what the call allocates), else the device's current stream."""
     if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"stream on {stream.device}, tensors on {t.device}")
+        if stream.device != dev:
+            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
         return torch.cuda.stream(stream)
-    if t.device.index != torch.cuda.current_device():
-        return torch.cuda.stream(torch.cuda.current_stream(t.device))
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.stream(torch.cuda.current_stream(dev))
     return _NO_SWITCH
 
 
-def _need_offsets(cu_seqlens):
-    _need(cu_seqlens, "cu_seqlens", dtype=torch.int32)
+# The current stream of a device as an integer; torch.cuda.current_stream() builds a Stream object
+# for it, 3.4 us of a 7 us call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _fit(t, name, shape, dtype, dev):
+    """_need for a tensor of known shape and dtype on a known device, quick when all is well (these
+    calls run once per layer and token, where the host's time is the step's)."""
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _need(t, name, shape, dtype)
+        raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+
+
+def _offsets_batch(cu_seqlens, dev):
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected (B + 1,)")
+    _fit(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
     return cu_seqlens.shape[0] - 1
 
 
 _KV_FORMATS = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _need_pages(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype):
-    """Checks the page pool; returns (n_pages, Hkv, d, format)."""
-    _need(k_pages, "k_pages")
-    if k_pages.dim() != 4 or k_pages.shape[2] != 64:
-        raise ValueError(f"k_pages has shape {tuple(k_pages.shape)}, expected (n_pages, Hkv, 64, d)")
-    _need(v_pages, "v_pages", k_pages.shape, k_pages.dtype)
-    _need(page_table, "page_table", dtype=torch.int32)
+def _code(dtype):
+    try:
+        return _DTYPES[dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)") from None
+
+
+def _pool(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype, dev):
+    """Checks the page pool; returns (n_pages, Hkv, d, format, pointers of the scales)."""
+    shape, kind = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or shape[2] != 64:
+        raise ValueError(f"k_pages has shape {tuple(shape)}, expected (n_pages, Hkv, 64, d)")
+    _fit(k_pages, "k_pages", shape, kind, dev)
+    _fit(v_pages, "v_pages", shape, kind, dev)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, max_pages)")
-    fmt = _KV_FORMATS.get(k_pages.dtype, KV_SAME)
+    _fit(page_table, "page_table", page_table.shape, torch.int32, dev)
+    fmt = _KV_FORMATS.get(kind, KV_SAME)
     if fmt == KV_SAME:
-        if k_pages.dtype != dtype:
-            raise ValueError(f"k_pages has dtype {k_pages.dtype}, expected {dtype}, int8 or float8_e4m3fn")
+        if kind != dtype:
+            raise ValueError(f"k_pages has dtype {kind}, expected {dtype}, int8 or float8_e4m3fn")
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale and v_scale belong to int8 and float8_e4m3fn pages")
-    else:
-        for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if s is None:
-                raise ValueError(f"{n} is needed for {k_pages.dtype} pages")
-            _need(s, n, k_pages.shape[:3], torch.float32)
-    return k_pages.shape[0], k_pages.shape[1], k_pages.shape[3], fmt
+        return shape[0], shape[1], shape[3], fmt, None, None
+    for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if s is None:
+            raise ValueError(f"{n} is needed for {kind} pages")
+        _fit(s, n, shape[:3], torch.float32, dev)
+    return shape[0], shape[1], shape[3], fmt, k_scale.data_ptr(), v_scale.data_ptr()
 
 
 def packed_prefill(q, k, v, cu_seqlens, o=None, scale=0.0, stream=None):
@@ -564,19 +583,22 @@ def packed_prefill(q, k, v, cu_seqlens, o=None, scale=0.0, stream=None):
     _need(q, "q")
     if q.dim() != 3:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected (H, total, d)")
-    H, total, d = q.shape
-    _need(k, "k", dtype=q.dtype)
-    if k.dim() != 3 or k.shape[1:] != q.shape[1:]:
+    (H, total, d), dtype, dev = q.shape, q.dtype, q.device
+    if k.dim() != 3 or k.shape[1:] != (total, d):
         raise ValueError(f"k has shape {tuple(k.shape)}, expected (Hkv, {total}, {d})")
-    _need(v, "v", k.shape, q.dtype)
-    B = _need_offsets(cu_seqlens)
-    _need(o, "o", q.shape, q.dtype)
-    with _on(q, stream, k, v, cu_seqlens, o):
+    _fit(k, "k", k.shape, dtype, dev)
+    _fit(v, "v", k.shape, dtype, dev)
+    B = _offsets_batch(cu_seqlens, dev)
+    code = _code(dtype)
+    with _on(dev, stream):
         if o is None:
             o = torch.empty_like(q)
-        _check(_lib.sala_packed_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(o), B, H,
-                                        k.shape[0], total, d, float(scale), _dt(q), _stream(stream)),
-               "sala_packed_prefill")
+        else:
+            _fit(o, "o", q.shape, dtype, dev)
+        r = _lib.sala_packed_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
+                                     o.data_ptr(), B, H, k.shape[0], total, d, scale, code,
+                                     _raw_stream(dev.index))
+    _check(r, "sala_packed_prefill")
     return o
 
 
@@ -589,17 +611,20 @@ def kv_write(k, v, cu_seqlens, pos, page_table, k_pages, v_pages, k_scale=None, 
     _need(k, "k")
     if k.dim() != 3:
         raise ValueError(f"k has shape {tuple(k.shape)}, expected (Hkv, total, d)")
-    _need(v, "v", k.shape, k.dtype)
-    B = _need_offsets(cu_seqlens)
-    _need(pos, "pos", (B,), torch.int32)
-    n_pages, Hkv, d, fmt = _need_pages(k_pages, v_pages, page_table, k_scale, v_scale, B, k.dtype)
-    if (k.shape[0], k.shape[2]) != (Hkv, d):
+    (Hk, total, dk), dtype, dev = k.shape, k.dtype, k.device
+    _fit(v, "v", k.shape, dtype, dev)
+    B = _offsets_batch(cu_seqlens, dev)
+    _fit(pos, "pos", (B,), torch.int32, dev)
+    n_pages, Hkv, d, fmt, ks, vs = _pool(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype, dev)
+    if Hk != Hkv or dk != d:
         raise ValueError(f"k has shape {tuple(k.shape)}, the pages hold ({Hkv}, tokens, {d})")
-    with _on(k, stream, v, cu_seqlens, pos, page_table, k_pages, v_pages, k_scale, v_scale):
-        _check(_lib.sala_kv_write(_ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(pos), _ptr(page_table),
-                                  page_table.shape[1], _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-                                  _ptr(v_scale), n_pages, B, Hkv, k.shape[1], d, 64, fmt, _dt(k),
-                                  _stream(stream)), "sala_kv_write")
+    code = _code(dtype)
+    with _on(dev, stream):
+        r = _lib.sala_kv_write(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), pos.data_ptr(),
+                               page_table.data_ptr(), page_table.shape[1], k_pages.data_ptr(),
+                               v_pages.data_ptr(), ks, vs, n_pages, B, Hkv, total, d, 64, fmt, code,
+                               _raw_stream(dev.index))
+    _check(r, "sala_kv_write")
 
 
 def kv_read(k_pages, v_pages, page_table, cu_seqlens, pos, total, dtype, k_scale=None, v_scale=None,
@@ -607,20 +632,29 @@ def kv_read(k_pages, v_pages, page_table, cu_seqlens, pos, total, dtype, k_scale
     """Reads tokens pos[b] .. of each sequence back as packed rows of dtype, cu_seqlens[b + 1] -
     cu_seqlens[b] of them: the inverse of kv_write.  Returns (k, v), [Hkv, total, d] each; rows
     behind cu_seqlens[B] are left as they were."""
-    B = _need_offsets(cu_seqlens)
-    _need(pos, "pos", (B,), torch.int32)
-    n_pages, Hkv, d, fmt = _need_pages(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype)
-    _need(k, "k", (Hkv, total, d), dtype)
-    _need(v, "v", (Hkv, total, d), dtype)
-    with _on(k_pages, stream, v_pages, page_table, cu_seqlens, pos, k_scale, v_scale, k, v):
+    _need(k_pages, "k_pages")
+    dev = k_pages.device
+    B = _offsets_batch(cu_seqlens, dev)
+    _fit(pos, "pos", (B,), torch.int32, dev)
+    n_pages, Hkv, d, fmt, ks, vs = _pool(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype, dev)
+    if not 0 <= total < 1 << 31:
+        raise ValueError(f"total {total} outside [0, 2^31)")
+    code = _code(dtype)
+    shape = (Hkv, total, d)
+    with _on(dev, stream):
         if k is None:
-            k = torch.empty((Hkv, total, d), dtype=dtype, device=k_pages.device)
+            k = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _fit(k, "k", shape, dtype, dev)
         if v is None:
-            v = torch.empty((Hkv, total, d), dtype=dtype, device=k_pages.device)
-        _check(_lib.sala_kv_read(_ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), n_pages,
-                                 _ptr(page_table), page_table.shape[1], _ptr(cu_seqlens), _ptr(pos),
-                                 _ptr(k), _ptr(v), B, Hkv, total, d, 64, fmt, _dt(k),
-                                 _stream(stream)), "sala_kv_read")
+            v = torch.empty_like(k)
+        else:
+            _fit(v, "v", shape, dtype, dev)
+        r = _lib.sala_kv_read(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, n_pages,
+                              page_table.data_ptr(), page_table.shape[1], cu_seqlens.data_ptr(),
+                              pos.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, total, d, 64, fmt,
+                              code, _raw_stream(dev.index))
+    _check(r, "sala_kv_read")
     return k, v
 
 
@@ -637,28 +671,31 @@ def tree_decode_paged(q, k_pages, v_pages, page_table, ctx, max_ctx, tree, k_sca
     _need(q, "q")
     if q.dim() != 4:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected (B, H, T, d)")
-    B, H, T, d = q.shape
-    n_pages, Hkv, dp, fmt = _need_pages(k_pages, v_pages, page_table, k_scale, v_scale, B, q.dtype)
+    (B, H, T, d), dtype, dev = q.shape, q.dtype, q.device
+    n_pages, Hkv, dp, fmt, ks, vs = _pool(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype, dev)
     if dp != d:
         raise ValueError(f"q has head dim {d}, the pages {dp}")
-    if not 0 <= int(max_ctx) < 1 << 31:
+    if not 0 <= max_ctx < 1 << 31:
         raise ValueError(f"max_ctx {max_ctx} outside [0, 2^31)")
-    _need(ctx, "ctx", (B,), torch.int32)
-    _need(tree, "tree", (B, T), torch.int64)
-    _need(o, "o", q.shape, q.dtype)
-    _need(workspace, "workspace", dtype=torch.uint8)
-    with _on(q, stream, k_pages, v_pages, page_table, ctx, tree, k_scale, v_scale, o, workspace):
+    _fit(ctx, "ctx", (B,), torch.int32, dev)
+    _fit(tree, "tree", (B, T), torch.int64, dev)
+    code = _code(dtype)
+    with _on(dev, stream):
         if o is None:
             o = torch.empty_like(q)
+        else:
+            _fit(o, "o", q.shape, dtype, dev)
         if workspace is None:
-            need = _lib.sala_tree_decode_paged_workspace(B, H, Hkv, T, int(max_ctx), d)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        _check(_lib.sala_tree_decode_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-                                           _ptr(v_scale), n_pages, _ptr(page_table),
-                                           page_table.shape[1], _ptr(ctx), int(max_ctx), _ptr(tree),
-                                           _ptr(o), B, H, Hkv, T, d, 64, float(scale),
-                                           _ptr(workspace), workspace.numel(), fmt, _dt(q),
-                                           _stream(stream)), "sala_tree_decode_paged")
+            need = _lib.sala_tree_decode_paged_workspace(B, H, Hkv, T, max_ctx, d)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        else:
+            _fit(workspace, "workspace", workspace.shape, torch.uint8, dev)
+        r = _lib.sala_tree_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
+                                        n_pages, page_table.data_ptr(), page_table.shape[1],
+                                        ctx.data_ptr(), max_ctx, tree.data_ptr(), o.data_ptr(), B, H,
+                                        Hkv, T, d, 64, scale, workspace.data_ptr(), workspace.numel(),
+                                        fmt, code, _raw_stream(dev.index))
+    _check(r, "sala_tree_decode_paged")
     return o
 
 
