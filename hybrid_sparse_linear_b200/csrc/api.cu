@@ -1011,6 +1011,10 @@ sala_status sala_tree_decode_paged(const void* q, const void* k_pages, const voi
     if ((s = get_ctx(&ctx)) != SALA_OK) return s;
     const sala::KvPages p{k_pages, v_pages, k_scale, v_scale, page_table, max_pages, n_pages};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dt == SALA_BF16 && sala::tree_mma_supported(H / Hkv * T))
+        return launched(sala::launch_tree_mma((sala::KvFormat)fmt, q, p, tree, o, ctx_len, max_ctx, B, H, Hkv,
+                                              T, d, scale, workspace, st, ctx),
+                        "tree_decode_paged_mma");
     if (dt == SALA_BF16)
         return launched(sala::launch_tree_tc((sala::KvFormat)fmt, q, p, tree, o, ctx_len, max_ctx, B, H, Hkv,
                                              T, d, scale, workspace, st, ctx),

@@ -214,6 +214,11 @@ size_t tree_simt_workspace(int rows, int d);
 cudaError_t launch_tree_simt(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
                              const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
                              float scale, void* ws, cudaStream_t st, DevCtx ctx);
+// At most 16 rows: warp-level tensor-core tiles (ws as below).
+bool tree_mma_supported(int rows);
+cudaError_t launch_tree_mma(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
+                            const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
+                            float scale, void* ws, cudaStream_t st, DevCtx ctx);
 size_t tree_tc_workspace(int rows, int d);
 cudaError_t launch_tree_tc(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
                            const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,

@@ -71,6 +71,35 @@ __device__ __forceinline__ float4 decode4(uint32_t c) {
     }
 }
 
+// Two codes as a bf16 pair, exactly (a code has at most 8 significant bits).  u holds a code in each 16
+// bits: in the low byte for Int8 (the other zero), in the high byte for E4M3 (the other ignored).
+template <KvFormat F>
+__device__ __forceinline__ uint32_t code_pair(uint32_t u) {
+    if constexpr (F == KvFormat::Int8) {
+        // For a byte b, 128 + (b & 127) and 128 or 256 (bit 7 is the last exponent bit of 0x4300 = 128)
+        // are bf16 numbers, and their difference is the signed byte.
+        const uint32_t x = (u & 0x007f007fu) | 0x43004300u, y = (u & 0x00800080u) | 0x43004300u;
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&y));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    } else {
+        // s eeee mmm moved to bf16's places is the value times 2^-120 (the biases differ by 120, and
+        // e4m3's subnormals become bf16's); the product with 2^120 is exact.
+        const uint32_t x = ((u >> 4) & 0x07f007f0u) | (u & 0x80008000u), k = 0x7b807b80u;
+        const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&k));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    }
+}
+// bf16 pairs of four codes in memory order.
+template <KvFormat F>
+__device__ __forceinline__ uint2 codes_to_bf16(uint32_t c) {
+    if constexpr (F == KvFormat::Int8)
+        return make_uint2(code_pair<F>(__byte_perm(c, 0u, 0x4140)), code_pair<F>(__byte_perm(c, 0u, 0x4342)));
+    else
+        return make_uint2(code_pair<F>(__byte_perm(c, 0u, 0x1404)), code_pair<F>(__byte_perm(c, 0u, 0x3424)));
+}
+
 // ---------------------------------------------------------------- packed sequences
 // Rows cu[b] .. cu[b + 1] of a packed tensor belong to sequence b.  A pair of offsets that does not
 // lie in order inside [0, total] counts as an empty sequence and sets *bad.

@@ -1,0 +1,477 @@
+// Attention of new tokens over a paged key/value cache for few query rows: at most 16 per KV head
+// (one token of a group of 16 heads), bf16 queries, the cache in bf16 or 8-bit codes.
+//
+// With 16 rows the step is the read of the cache: 64 d operations per key against 2 (d + 4) bytes in
+// 8 bits.  A 128-row tensor-core tile would be seven eighths empty, and its chain through shared
+// memory and TMEM costs more than the work, so each warp takes whole pages on its own: K and V of a
+// page land in the warp's own buffers by TMA (the next page's K is requested as soon as S is formed,
+// its V after P V), the products are m16n8k16 tiles, and codes become bf16 fragments in registers.
+// Twelve warps (six for bf16 rows of 256 bytes) keep about 150 KB per SM on their way.
+//
+// Fragments.  The contraction over d may take its elements in any order as long as Q and K agree: a
+// lane reads 16 bytes of a key's row and uses them for consecutive steps of four elements, and Q's
+// fragments are laid out to match.  The keys of an 8-key tile are dealt to the fragment's columns in
+// the order 0 4 1 5 2 6 3 7 where rows are 128 bytes, so that the lanes of a load phase fall into
+// different banks under the 128-byte swizzle; P's columns meet V's rows in the same order.  V comes
+// transposed (ldmatrix): of codes, two neighbouring columns at a time, split by byte.
+//
+// 8-bit scales, hidden positions, infinities and NaN: as in the tensor-core kernel (tree_tc.cu).  The
+// warps' accumulators are joined in shared memory at an item's end.
+#include <type_traits>
+
+#include "decode_common.cuh"
+#include "kv_format.cuh"
+#include "softmax_tile.cuh"
+#include "tmap.cuh"
+#include "tree_plan.cuh"
+
+namespace sala {
+namespace {
+
+using namespace ptx;
+using namespace smx;
+using namespace dec;
+
+constexpr int kRows = 16;
+
+template <int D, KvFormat F>
+struct Layout {
+    static constexpr bool kCodes = F != KvFormat::Same;
+    static constexpr int kRowBytes = D * (kCodes ? 1 : 2);
+    static constexpr int kBoxBytes = kRowBytes < 128 ? kRowBytes : 128;  // of a row, per TMA box
+    static constexpr int kBoxes = kRowBytes / kBoxBytes;
+    static constexpr int kTile = kPage * kRowBytes;                      // K or V of a page
+    static constexpr int kWarps = kRowBytes > 128 ? 6 : 12;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kStage = 2 * kTile;                             // a warp's K and V
+    static constexpr int kOffScale = kWarps * kStage;                    // [warp][k, v][64]
+    static constexpr int kOffNotes = kOffScale + (kCodes ? kWarps * 2 * kPage * 4 : 0);
+    static constexpr int kOffMl = kOffNotes + (kCodes ? 0 : 2 * D * 8);  // [warp][16] (maximum, sum)
+    static constexpr int kOffBars = kOffMl + kWarps * kRows * 8;
+    static constexpr int kBytes = kOffBars + kWarps * 2 * 8;
+    static_assert(kRows * D * 4 <= kStage, "a warp's accumulator goes into its buffers");
+};
+
+// 16-byte piece c of row r of a tile whose boxes are swizzled.
+template <class L>
+__device__ __forceinline__ uint8_t* piece(uint8_t* tile, int r, int c) {
+    if constexpr (L::kBoxBytes == 128)
+        return tile + (c >> 3) * (kPage * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    else
+        return tile + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+// Key of an 8-key tile in fragment column n.
+template <class L>
+__device__ __forceinline__ int key_of(int n) {
+    return L::kBoxBytes == 128 ? (n & 1) * 4 + (n >> 1) : n;
+}
+
+template <int D, KvFormat F>
+__global__ void __launch_bounds__(Layout<D, F>::kThreads, 1)
+tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                const __nv_bfloat16* __restrict__ q, KvPages pages, const uint64_t* __restrict__ masks,
+                __nv_bfloat16* __restrict__ out, tree::Shape s, tree::Partials part, bool by_item, float sl2,
+                DevCtx ctx) {
+    using L = Layout<D, F>;
+    constexpr bool kCodes = L::kCodes;
+    constexpr int kPer = kCodes ? 16 : 8;     // elements in 16 bytes
+    constexpr int kPieces = D / kPer;         // per row
+    constexpr int kSteps = D / 16;            // of the contraction over d
+    extern __shared__ __align__(1024) uint8_t sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;    // fragment row (and row + 8), column pair
+    uint8_t* K = sm + warp * L::kStage;
+    uint8_t* V = K + L::kTile;
+    float* ksc = reinterpret_cast<float*>(sm + L::kOffScale) + warp * 2 * kPage;
+    float* vsc = ksc + kPage;
+    unsigned long long* notes = reinterpret_cast<unsigned long long*>(sm + L::kOffNotes);
+    float2* ml = reinterpret_cast<float2*>(sm + L::kOffMl);
+    uint64_t* kbar = reinterpret_cast<uint64_t*>(sm + L::kOffBars) + warp * 2;
+    uint64_t* vbar = kbar + 1;
+    __shared__ tree::Cursor cur0;
+    __shared__ int noted;
+
+    cudaTriggerProgrammaticLaunchCompletion();  // the join may be set up; it waits for this grid's end
+    if (lane == 0) {
+        mbar_init(kbar, 1);
+        mbar_init(vbar, 1);
+        fence_mbar_init();
+    }
+    if (by_item) {
+        if (tid == 0) {
+            tree::Cursor c;
+            bool bad = false;
+            c.b = blockIdx.x / s.Hkv;
+            c.g = blockIdx.x % s.Hkv;
+            c.rt = c.tile = 0;
+            c.ctx = tree::ctx_of(s, c.b, &bad);
+            c.n_tiles = tree::tiles_of(s, c.ctx);
+            c.left = c.n_tiles;
+            cur0 = c;
+            if (bad) flag(ctx, kStatusBounds);
+        }
+    } else if (warp == 0) {
+        bool bad = false;
+        const long long w = tree::total_tiles(s, lane, &bad);
+        if (bad && blockIdx.x == 0) flag(ctx, kStatusBounds);
+        const long long x0 = tree::run_start(w, blockIdx.x, gridDim.x);
+        const tree::Cursor c = tree::find_tile(s, x0, tree::run_start(w, blockIdx.x + 1, gridDim.x) - x0, lane);
+        if (lane == 0) cur0 = c;
+    }
+    __syncthreads();
+    tree::Cursor c = cur0;
+    uint32_t nk = 0, nv = 0;  // loads requested so far
+    bool dead = false;        // a wait ran out: no more loads
+
+    for (bool first = true; c.left > 0; tree::next_item(s, c), first = false) {
+        const int n = tree::run_tiles(c), end = c.tile + n;
+        const int64_t row0 = ((int64_t)c.b * s.Hkv + c.g) * s.rows;
+        // This warp takes the run's pages warp, warp + kWarps, ...; lane i knows the page of the next
+        // 32 of them that is its own i-th.
+        int ids = -1, ids_at = -32;
+        auto page_at = [&](int i) {  // converged; -1: left out, or past the end
+            if (i >= ids_at + 32) {
+                ids_at = i;
+                const int tl = c.tile + warp + L::kWarps * (i + lane);
+                ids = tl < end ? page_of(pages, c.b, tl) : -1;
+                if (tl < end && ids < 0) flag(ctx, kStatusBounds);
+            }
+            return __shfl_sync(0xffffffffu, ids, i - ids_at);
+        };
+        auto load = [&](int id, bool is_k) {
+            if (id < 0 || dead) return;
+            if (lane == 0) {
+                uint64_t* bar = is_k ? kbar : vbar;
+                const int row = (id * s.Hkv + c.g) * kPage;
+                mbar_arrive_expect_tx(bar, L::kTile + (kCodes ? kPage * 4 : 0));
+                for (int x = 0; x < L::kBoxes; ++x)
+                    tma_load_2d((is_k ? K : V) + x * kPage * L::kBoxBytes, is_k ? &tmK : &tmV, bar,
+                                x * (L::kBoxBytes / (kCodes ? 1 : 2)), row);
+                if constexpr (kCodes)
+                    bulk_load_g2s(is_k ? ksc : vsc, (is_k ? pages.k_scale : pages.v_scale) + row, kPage * 4, bar);
+            }
+            if (is_k) ++nk;
+            else ++nv;
+        };
+        const int n_my = (n - warp + L::kWarps - 1) / L::kWarps;  // may be <= 0
+        int id = n_my > 0 ? page_at(0) : -1;
+        load(id, true);
+        load(id, false);
+
+        // Q's fragments and the rows' draft masks.
+        uint32_t qa[kSteps][4];
+        uint64_t bits[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = g + 8 * h;
+            const bool real = r < s.rows;
+            bits[h] = real ? tree::draft_bits(masks, c.b, r % s.T, s.T) : 0ull;
+            const __nv_bfloat16* src = q + (row0 + r) * D + t * kPer;
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st) {
+                const uint2 u = real ? __ldg(reinterpret_cast<const uint2*>(
+                                           src + (st / (kPer / 4)) * 4 * kPer + (st % (kPer / 4)) * 4))
+                                     : make_uint2(0u, 0u);
+                qa[st][h] = u.x;
+                qa[st][2 + h] = u.y;
+            }
+        }
+        if constexpr (!kCodes) {
+            if (tid == 0) noted = 0;
+            for (int e = tid; e < 2 * D; e += L::kThreads) notes[e] = 0ull;
+            __syncthreads();
+        }
+        RowState st[2];
+        float o[D / 8][4];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+
+        for (int i = 0; i < n_my; ++i) {
+            const int next = i + 1 < n_my ? page_at(i + 1) : -1;
+            const int k0 = (c.tile + warp + L::kWarps * i) * kPage;
+            if (id < 0) {
+                id = next;
+                load(id, true);
+                load(id, false);
+                continue;
+            }
+            if (!dead && !__all_sync(0xffffffffu, mbar_wait(kbar, (nk - 1) & 1, ctx))) dead = true;
+            if (dead) break;
+            float sc[8][4];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+                const int r = 8 * j + key_of<L>(g);
+#pragma unroll
+                for (int p = 0; p < kPieces / 4; ++p) {
+                    const uint4 u = ld16(piece<L>(K, r, 4 * p + t));
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                    if constexpr (kCodes) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint2 b = codes_to_bf16<F>(w[x]);
+                            mma16816(sc[j], qa[4 * p + x], {b.x, b.y});
+                        }
+                    } else {
+                        mma16816(sc[j], qa[2 * p], {w[0], w[1]});
+                        mma16816(sc[j], qa[2 * p + 1], {w[2], w[3]});
+                    }
+                }
+            }
+            if constexpr (kCodes) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float a = ksc[8 * j + key_of<L>(2 * t)], b = ksc[8 * j + key_of<L>(2 * t + 1)];
+                    sc[j][0] *= a;
+                    sc[j][1] *= b;
+                    sc[j][2] *= a;
+                    sc[j][3] *= b;
+                }
+            }
+            __syncwarp();
+            load(next, true);
+            const bool tail = k0 + kPage > c.ctx;
+            uint32_t seen[2] = {0xffffffffu, 0xffffffffu};  // per row: bit 2 j + i of this lane's columns
+            if (tail) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    seen[h] = 0u;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const int dr = k0 + 8 * j + key_of<L>(2 * t + x) - c.ctx;  // draft number
+                            if (dr < 0 || (dr < 64 && ((bits[h] >> dr) & 1ull))) seen[h] |= 1u << (2 * j + x);
+                        }
+                }
+            }
+            float alpha[2], nb[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (!tail || ((seen[h] >> (2 * j + x)) & 1u)) mx = max2n(mx, sc[j][2 * h + x]);
+                mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                alpha[h] = st[h].raise(mx * sl2);
+                nb[h] = st[h].shift();
+            }
+            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                for (int e = 0; e < D / 8; ++e) {
+                    o[e][0] *= alpha[0];
+                    o[e][1] *= alpha[0];
+                    o[e][2] *= alpha[1];
+                    o[e][3] *= alpha[1];
+                }
+            }
+            if (!__all_sync(0xffffffffu, mbar_wait(vbar, (nv - 1) & 1, ctx))) {
+                dead = true;
+                break;
+            }
+            if constexpr (!kCodes) {
+                if (tail) {  // V's rows that not every row sees: see tree_tc.cu
+                    constexpr int kC = D / 8;
+                    for (int e = lane; e < kPage * kC; e += 32) {
+                        const int r = e / kC, p = e % kC, dr = k0 + r - c.ctx;
+                        uint4* u = reinterpret_cast<uint4*>(piece<L>(V, r, p));
+                        if (dr >= s.T) {
+                            *u = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (dr >= 0 && any_nonfinite8(*u)) {
+                            uint16_t* w = reinterpret_cast<uint16_t*>(u);
+                            for (int x = 0; x < 8; ++x) {
+                                if ((w[x] & 0x7f80u) != 0x7f80u) continue;
+                                const bool nan = (w[x] & 0x7fu) != 0u, neg = (w[x] & 0x8000u) != 0u;
+                                if (nan || !neg) atomicOr(notes + p * 8 + x, 1ull << dr);
+                                if (nan || neg) atomicOr(notes + D + p * 8 + x, 1ull << dr);
+                                w[x] = 0;
+                            }
+                            noted = 1;
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                uint32_t pa[4];
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int j = 2 * jj + y;
+                    float va = 1.f, vb = 1.f;
+                    if constexpr (kCodes) {
+                        va = vsc[8 * j + key_of<L>(2 * t)];
+                        vb = vsc[8 * j + key_of<L>(2 * t + 1)];
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float p0 = ex2(fmaf(sc[j][2 * h], sl2, nb[h])), p1 = ex2(fmaf(sc[j][2 * h + 1], sl2, nb[h]));
+                        const bool s0 = !tail || ((seen[h] >> (2 * j)) & 1u), s1 = !tail || ((seen[h] >> (2 * j + 1)) & 1u);
+                        st[h].l += (s0 ? p0 : 0.f) + (s1 ? p1 : 0.f);
+                        if constexpr (kCodes) {
+                            p0 *= va;
+                            p1 *= vb;
+                        }
+                        pa[2 * y + h] = pack_bf16x2(s0 ? p0 : 0.f, s1 ? p1 : 0.f);
+                    }
+                }
+                // lanes 8 m .. 8 m + 7 address matrix m: 8 keys of tile 2 jj + (m & 1), piece p + (m >> 1)
+                const int vr = 8 * (2 * jj + ((lane >> 3) & 1)) + key_of<L>(lane & 7);
+#pragma unroll
+                for (int p = 0; p < kPieces; p += 2) {
+                    uint32_t u[4];
+                    ldsm_x4_t(u, piece<L>(V, vr, p + (lane >> 4)));
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint32_t a = u[2 * y], b = u[2 * y + 1];
+                        if constexpr (F == KvFormat::Int8) {
+                            mma16816(o[2 * (p + y)], pa, {code_pair<F>(__byte_perm(a, 0u, 0x4240)), code_pair<F>(__byte_perm(b, 0u, 0x4240))});
+                            mma16816(o[2 * (p + y) + 1], pa, {code_pair<F>(__byte_perm(a, 0u, 0x4341)), code_pair<F>(__byte_perm(b, 0u, 0x4341))});
+                        } else if constexpr (F == KvFormat::E4M3) {
+                            mma16816(o[2 * (p + y)], pa, {code_pair<F>(__byte_perm(a, 0u, 0x2404)), code_pair<F>(__byte_perm(b, 0u, 0x2404))});
+                            mma16816(o[2 * (p + y) + 1], pa, {code_pair<F>(__byte_perm(a, 0u, 0x3414)), code_pair<F>(__byte_perm(b, 0u, 0x3414))});
+                        } else {
+                            mma16816(o[p + y], pa, {a, b});
+                        }
+                    }
+                }
+            }
+            if (!kCodes && tail) fence_proxy_async_smem();  // the next copy comes behind the zeros
+            __syncwarp();
+            id = next;
+            load(id, false);
+        }
+
+        // The warp's partial into its own buffers (every load of the item has landed and is used).
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float l = st[h].l;
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if (t == 0) ml[warp * kRows + g + 8 * h] = make_float2(st[h].m, l);
+            float* dst = reinterpret_cast<float*>(K) + (g + 8 * h) * D;
+            if (n_my > 0 && !dead) {
+                if constexpr (kCodes) {  // tiles 2 p and 2 p + 1: columns 16 p + 4 t + 0, 2 and 1, 3
+#pragma unroll
+                    for (int p = 0; p < kPieces; ++p)
+                        *reinterpret_cast<float4*>(dst + 16 * p + 4 * t) =
+                            make_float4(o[2 * p][2 * h], o[2 * p + 1][2 * h], o[2 * p][2 * h + 1], o[2 * p + 1][2 * h + 1]);
+                } else {
+#pragma unroll
+                    for (int p = 0; p < D / 8; ++p)
+                        *reinterpret_cast<float2*>(dst + 8 * p + 2 * t) = make_float2(o[p][2 * h], o[p][2 * h + 1]);
+                }
+            }
+        }
+        const bool lost = __syncthreads_or(dead);
+        if (lost) break;
+        const bool whole = c.tile == 0 && n == c.n_tiles;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * s.rows;
+        for (int e = tid; e < s.rows * (D / 4); e += L::kThreads) {
+            const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < L::kWarps; ++w) top = fmaxf(top, ml[w * kRows + r].x);
+            float l = 0.f;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < L::kWarps; ++w) {
+                const float2 p = ml[w * kRows + r];
+                if (p.x == -INFINITY && p.y == 0.f) continue;  // saw nothing
+                const float wt = ex2(p.x - top);
+                const float4 y = *reinterpret_cast<const float4*>(sm + w * L::kStage + (r * D + col) * 4);
+                l += wt * p.y;
+                x.x += wt * y.x;
+                x.y += wt * y.y;
+                x.z += wt * y.z;
+                x.w += wt * y.w;
+            }
+            if constexpr (!kCodes) {
+                if (noted) {  // rows that attend to a draft with an infinity or a NaN in V get it back
+                    const uint64_t b = tree::draft_bits(masks, c.b, r % s.T, s.T);
+                    float* f = &x.x;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (notes[col + j] & b) f[j] += INFINITY;
+                        if (notes[D + col + j] & b) f[j] -= INFINITY;
+                    }
+                }
+            }
+            if (whole) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                *reinterpret_cast<uint2*>(out + (row0 + r) * D + col) =
+                    make_uint2(pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+            } else {
+                if (col == 0) part.ml[slot + r] = make_float2(top, l);
+                *reinterpret_cast<float4*>(part.o + (slot + r) * D + col) = x;
+            }
+        }
+        fence_proxy_async_smem();  // the next item's copies come behind what was written here
+        __syncthreads();
+    }
+    // Copies that a wind-down left on their way land before the block exits.
+    if (dead && lane == 0) {
+        if (nk > 0) (void)mbar_wait(kbar, (nk - 1) & 1, ctx);
+        if (nv > 0) (void)mbar_wait(vbar, (nv - 1) & 1, ctx);
+    }
+}
+
+// Short contexts: a block per item, with no partials to join, where its warps have a few pages each.
+constexpr int kItemPages = 24;
+
+template <int D, KvFormat F>
+cudaError_t tree_mma(const void* q, const KvPages& pages, const uint64_t* masks, void* o, tree::Shape s,
+                     void* ws, float scale, cudaStream_t st, DevCtx ctx) {
+    using L = Layout<D, F>;
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return cudaErrorNotSupported;
+    CUtensorMap tmK{}, tmV{};
+    auto map = [&](CUtensorMap* m, const void* base) {
+        cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)pages.n_pages * s.Hkv * kPage};
+        cuuint64_t strides[1] = {(cuuint64_t)L::kRowBytes};
+        cuuint32_t box[2] = {(cuuint32_t)(L::kBoxBytes / (L::kCodes ? 1 : 2)), (cuuint32_t)kPage};
+        cuuint32_t one[2] = {1, 1};
+        return fn(m, L::kCodes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                  const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  L::kBoxBytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (pages.n_pages > 0 && (!map(&tmK, pages.k) || !map(&tmV, pages.v))) return cudaErrorInvalidValue;
+    if (cudaError_t e = ensure_smem<tree_mma_kernel<D, F>>(L::kBytes); e != cudaSuccess) return e;
+    const int tiles = (s.max_ctx + s.T + kPage - 1) / kPage;
+    const bool by_item = tiles <= kItemPages;
+    const long long most = (long long)s.B * s.Hkv * tiles;
+    const int sms = device_sm_count();
+    const int n_cta = by_item ? s.B * s.Hkv : most < sms ? (int)most : sms;
+    const tree::Partials part = tree::partials_at(ws, by_item ? 0 : n_cta, s.rows);
+    tree_mma_kernel<D, F><<<n_cta, L::kThreads, L::kBytes, st>>>(
+        tmK, tmV, static_cast<const __nv_bfloat16*>(q), pages, masks, static_cast<__nv_bfloat16*>(o), s,
+        part, by_item, scale * 1.4426950408889634f, ctx);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (by_item) return cudaSuccess;
+    return launch_tree_join(DType::BF16, part, o, s, s.rows, D, n_cta, st);
+}
+
+}  // namespace
+
+bool tree_mma_supported(int rows) { return rows <= kRows; }
+
+cudaError_t launch_tree_mma(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
+                            const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
+                            float scale, void* ws, cudaStream_t st, DevCtx ctx) {
+    const tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, H / Hkv * T, 1, kPage};
+    auto go = [&](auto dd) {
+        constexpr int D = decltype(dd)::value;
+        if (f == KvFormat::Int8) return tree_mma<D, KvFormat::Int8>(q, pages, masks, o, s, ws, scale, st, ctx);
+        if (f == KvFormat::E4M3) return tree_mma<D, KvFormat::E4M3>(q, pages, masks, o, s, ws, scale, st, ctx);
+        return tree_mma<D, KvFormat::Same>(q, pages, masks, o, s, ws, scale, st, ctx);
+    };
+    return d == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
+}
+
+}  // namespace sala

@@ -96,33 +96,6 @@ struct Bars {
     int abort;
 };
 
-// bf16 pairs of four codes.
-template <KvFormat F>
-__device__ __forceinline__ uint2 codes_to_bf16(uint32_t c) {
-    if constexpr (F == KvFormat::Int8) {
-        // A byte u in 16 bits: 128 + (u & 127) and 128 or 256 (bit 7 is the last exponent bit of
-        // 0x4300 = 128) are bf16 numbers, and their difference is the signed byte, exactly.
-        auto two = [](uint32_t u) {
-            const uint32_t a = (u & 0x007f007fu) | 0x43004300u, b = (u & 0x00800080u) | 0x43004300u;
-            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                             *reinterpret_cast<const __nv_bfloat162*>(&b));
-            return *reinterpret_cast<const uint32_t*>(&d);
-        };
-        return make_uint2(two(__byte_perm(c, 0u, 0x4140)), two(__byte_perm(c, 0u, 0x4342)));
-    } else {
-        // s eeee mmm moved to bf16's places is the value times 2^-120 (the biases differ by 120, and
-        // e4m3's subnormals become bf16's); the product with 2^120 is exact.
-        const uint32_t k = 0x7b807b80u;  // 2^120
-        auto two = [&](uint32_t h) {     // the byte in the high half of each 16 bits
-            const uint32_t a = ((h >> 4) & 0x07f007f0u) | (h & 0x80008000u);
-            const __nv_bfloat162 d = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                             *reinterpret_cast<const __nv_bfloat162*>(&k));
-            return *reinterpret_cast<const uint32_t*>(&d);
-        };
-        return make_uint2(two(__byte_perm(c, 0u, 0x1404)), two(__byte_perm(c, 0u, 0x3424)));
-    }
-}
-
 template <int D, KvFormat F, bool kWide>
 __global__ void __launch_bounds__(Layout<D, F, kWide>::kThreads, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
