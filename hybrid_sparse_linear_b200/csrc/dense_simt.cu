@@ -24,6 +24,7 @@ constexpr int kRows = 64;   // query rows per block
 constexpr int kKeys = 64;   // keys per tile: one page of the paged cache
 constexpr int kThreads = 256;
 constexpr int kPad = 4;     // floats: 16-byte rows that start 4 banks apart
+constexpr int kPad0 = 1;    // beginning an item costs about a tile
 constexpr float kHidden = -1.f;  // P of a position its row does not see (probabilities are >= 0)
 
 template <int D>
@@ -220,10 +221,10 @@ tree_simt_kernel(const float* __restrict__ q, KvPages pages, const uint64_t* __r
     const int tid = threadIdx.x;
     if (tid < 32) {
         bool bad = false;
-        const long long w = tree::total_tiles(s, tid, &bad);
+        const long long w = tree::total_places(s, tid, &bad);
         const long long x0 = tree::run_start(w, blockIdx.x, gridDim.x);
         const long long x1 = tree::run_start(w, blockIdx.x + 1, gridDim.x);
-        const tree::Cursor c = tree::find_tile(s, x0, x1 - x0, tid);
+        const tree::Cursor c = tree::find_place(s, x0, x1 - x0, tid);
         if (bad && blockIdx.x == 0) flag(ctx, kStatusBounds);
         if (tid == 0) cur0 = c;
     }
@@ -231,9 +232,10 @@ tree_simt_kernel(const float* __restrict__ q, KvPages pages, const uint64_t* __r
     tree::Cursor c = cur0;
     constexpr int kLd = D + kPad;
     const int ty = tid >> 4, tx = tid & 15;
-    for (bool first = true; c.left > 0; tree::next_item(s, c), first = false) {
+    for (; c.left > 0; tree::next_item(s, c)) {
         const int r0 = c.rt * kRows, n_rows = min(kRows, s.rows - r0);
-        const int n = tree::run_tiles(c);
+        const int n = tree::run_tiles(c), t0 = tree::first_tile(c);
+        if (n == 0) continue;
         const int64_t row0 = ((int64_t)c.b * s.Hkv + c.g) * s.rows + r0;
         __syncthreads();  // the previous item is done with Q and bits
         for (int e = tid; e < kRows * (D / 4); e += kThreads) {
@@ -245,7 +247,7 @@ tree_simt_kernel(const float* __restrict__ q, KvPages pages, const uint64_t* __r
         __syncthreads();
         Rows<D> st;
         st.clear();
-        for (int t = c.tile; t < c.tile + n; ++t) {
+        for (int t = t0; t < t0 + n; ++t) {
             const int k0 = t * kKeys;
             const int page = page_of(pages, c.b, t);
             if (page < 0) {  // a page the table does not hold: its keys are left out
@@ -265,8 +267,8 @@ tree_simt_kernel(const float* __restrict__ q, KvPages pages, const uint64_t* __r
                                return j < 0 || (j < s.T && ((bits[row] >> j) & 1ull));
                            });
         }
-        const bool whole = c.tile == 0 && n == c.n_tiles;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * min(s.rows, kRows);
+        const bool whole = n == c.n_tiles;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * min(s.rows, kRows);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = ty * 4 + i;
@@ -330,7 +332,7 @@ cudaError_t launch_tree_simt(KvFormat f, const void* q, const KvPages& pages, co
                              const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
                              float scale, void* ws, cudaStream_t st, DevCtx ctx) {
     const int rows = H / Hkv * T;
-    const tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, rows, tree::row_tiles(rows, kRows), kKeys};
+    const tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, rows, tree::row_tiles(rows, kRows), kKeys, kPad0};
     auto go = [&](auto dd) {
         constexpr int D = decltype(dd)::value;
         if (f == KvFormat::Int8) return tree_simt<D, KvFormat::Int8>(q, pages, masks, o, s, ws, scale, st, ctx);

@@ -25,7 +25,7 @@ tree_join_kernel(tree::Partials part, T* __restrict__ out, tree::Shape s, int rt
     // where the group's items start in the line of tiles
     long long w = 0, before = 0;
     for (int i = lane; i < s.B; i += 32) {
-        const int n = tree::tiles_of(s, tree::ctx_of(s, i));
+        const int n = tree::places_of(s, tree::ctx_of(s, i));
         w += n;
         if (i < b) before += n;
     }
@@ -39,14 +39,11 @@ tree_join_kernel(tree::Partials part, T* __restrict__ out, tree::Shape s, int rt
     const int n_tiles = tree::tiles_of(s, tree::ctx_of(s, b));
     for (int row = blockIdx.x * kWarps + (threadIdx.x >> 5); row < s.rows; row += gridDim.x * kWarps) {
         const int r_tile = row / rt;
-        const long long x0 = before * per + ((long long)g * s.n_rt + r_tile) * n_tiles;
-        const long long x1 = x0 + n_tiles;
+        const long long x0 = before * per + ((long long)g * s.n_rt + r_tile) * (n_tiles + s.pad) + s.pad;
+        const long long x1 = x0 + n_tiles;  // the item's tiles
         const int c0 = tree::run_of(w, x0, n_cta), c1 = tree::run_of(w, x1 - 1, n_cta);
         if (c0 == c1) continue;  // one CTA had the item whole and wrote the row
-        auto slot = [&](int c) {
-            const bool later = c == c0 && tree::run_start(w, c, n_cta) < x0;
-            return ((size_t)c * 2 + (later ? 1 : 0)) * rt + row % rt;
-        };
+        auto slot = [&](int c) { return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * rt + row % rt; };
         // A CTA between the two whose run is empty (fewer tiles than CTAs) left nothing.
         auto empty = [&](int c) { return tree::run_start(w, c, n_cta) == tree::run_start(w, c + 1, n_cta); };
         float m = -INFINITY;
@@ -75,16 +72,28 @@ tree_join_kernel(tree::Partials part, T* __restrict__ out, tree::Shape s, int rt
                     lc = ml.y * wt;
                 }
             }
-            for (unsigned left = __ballot_sync(0xffffffffu, seen); left; left &= left - 1) {
-                const int i = __ffs((int)left) - 1;
-                const float wi = __shfl_sync(0xffffffffu, wt, i);
-                l += __shfl_sync(0xffffffffu, lc, i);
-                const float* src = part.o + slot(base + i) * D + lane * kC;
+            // Eight at a time, so that their reads are on the way together.
+            const unsigned who = __ballot_sync(0xffffffffu, seen);
+            const int n = min(32, c1 - base + 1);
+            for (int i0 = 0; i0 < n; i0 += 8) {
+                float2 x[8][kC / 2];
 #pragma unroll
-                for (int e = 0; e < kC; e += 2) {
-                    const float2 x = *reinterpret_cast<const float2*>(src + e);
-                    acc[e] += wi * x.x;
-                    acc[e + 1] += wi * x.y;
+                for (int i = 0; i < 8; ++i) {
+                    const bool take = (who >> (i0 + i)) & 1u;
+                    const float* src = part.o + slot(base + i0 + i) * D + lane * kC;
+#pragma unroll
+                    for (int e = 0; e < kC / 2; ++e)
+                        x[i][e] = take ? reinterpret_cast<const float2*>(src)[e] : make_float2(0.f, 0.f);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float wi = __shfl_sync(0xffffffffu, wt, (i0 + i) & 31);
+                    l += __shfl_sync(0xffffffffu, lc, (i0 + i) & 31);
+#pragma unroll
+                    for (int e = 0; e < kC / 2; ++e) {
+                        acc[2 * e] += wi * x[i][e].x;
+                        acc[2 * e + 1] += wi * x[i][e].y;
+                    }
                 }
             }
         }

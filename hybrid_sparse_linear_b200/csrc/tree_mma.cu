@@ -112,10 +112,10 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
     } else if (warp == 0) {
         bool bad = false;
-        const long long w = tree::total_tiles(s, lane, &bad);
+        const long long w = tree::total_places(s, lane, &bad);
         if (bad && blockIdx.x == 0) flag(ctx, kStatusBounds);
         const long long x0 = tree::run_start(w, blockIdx.x, gridDim.x);
-        const tree::Cursor c = tree::find_tile(s, x0, tree::run_start(w, blockIdx.x + 1, gridDim.x) - x0, lane);
+        const tree::Cursor c = tree::find_place(s, x0, tree::run_start(w, blockIdx.x + 1, gridDim.x) - x0, lane);
         if (lane == 0) cur0 = c;
     }
     __syncthreads();
@@ -123,8 +123,9 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     uint32_t nk = 0, nv = 0;  // loads requested so far
     bool dead = false;        // a wait ran out: no more loads
 
-    for (bool first = true; c.left > 0; tree::next_item(s, c), first = false) {
-        const int n = tree::run_tiles(c), end = c.tile + n;
+    for (; c.left > 0; tree::next_item(s, c)) {
+        const int n = tree::run_tiles(c), t0 = tree::first_tile(c), end = t0 + n;
+        if (n == 0) continue;
         const int64_t row0 = ((int64_t)c.b * s.Hkv + c.g) * s.rows;
         // This warp takes the run's pages warp, warp + kWarps, ...; lane i knows the page of the next
         // 32 of them that is its own i-th.
@@ -132,7 +133,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         auto page_at = [&](int i) {  // converged; -1: left out, or past the end
             if (i >= ids_at + 32) {
                 ids_at = i;
-                const int tl = c.tile + warp + L::kWarps * (i + lane);
+                const int tl = t0 + warp + L::kWarps * (i + lane);
                 ids = tl < end ? page_of(pages, c.b, tl) : -1;
                 if (tl < end && ids < 0) flag(ctx, kStatusBounds);
             }
@@ -190,7 +191,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 
         for (int i = 0; i < n_my; ++i) {
             const int next = i + 1 < n_my ? page_at(i + 1) : -1;
-            const int k0 = (c.tile + warp + L::kWarps * i) * kPage;
+            const int k0 = (t0 + warp + L::kWarps * i) * kPage;
             if (id < 0) {
                 id = next;
                 load(id, true);
@@ -232,9 +233,11 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
             __syncwarp();
             load(next, true);
-            const bool tail = k0 + kPage > c.ctx;
+            // Softmax and P V, once for pages that every row sees whole and once for the others.
+            auto rest = [&](auto masked) -> bool {
+            constexpr bool tail = decltype(masked)::value;
             uint32_t seen[2] = {0xffffffffu, 0xffffffffu};  // per row: bit 2 j + i of this lane's columns
-            if (tail) {
+            if constexpr (tail) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     seen[h] = 0u;
@@ -252,10 +255,15 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             for (int h = 0; h < 2; ++h) {
                 float mx = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < 8; ++j) {
+                    if constexpr (!tail) {
+                        mx = max3n(mx, sc[j][2 * h], sc[j][2 * h + 1]);
+                    } else {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        if (!tail || ((seen[h] >> (2 * j + x)) & 1u)) mx = max2n(mx, sc[j][2 * h + x]);
+                        for (int x = 0; x < 2; ++x)
+                            if ((seen[h] >> (2 * j + x)) & 1u) mx = max2n(mx, sc[j][2 * h + x]);
+                    }
+                }
                 mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 alpha[h] = st[h].raise(mx * sl2);
@@ -272,10 +280,10 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
             if (!__all_sync(0xffffffffu, mbar_wait(vbar, (nv - 1) & 1, ctx))) {
                 dead = true;
-                break;
+                return false;
             }
             if constexpr (!kCodes) {
-                if (tail) {  // V's rows that not every row sees: see tree_tc.cu
+                if constexpr (tail) {  // V's rows that not every row sees: see tree_tc.cu
                     constexpr int kC = D / 8;
                     for (int e = lane; e < kPage * kC; e += 32) {
                         const int r = e / kC, p = e % kC, dr = k0 + r - c.ctx;
@@ -303,7 +311,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int j = 2 * jj + y;
-                    float va = 1.f, vb = 1.f;
+                    [[maybe_unused]] float va = 1.f, vb = 1.f;
                     if constexpr (kCodes) {
                         va = vsc[8 * j + key_of<L>(2 * t)];
                         vb = vsc[8 * j + key_of<L>(2 * t + 1)];
@@ -342,6 +350,9 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
             }
             if (!kCodes && tail) fence_proxy_async_smem();  // the next copy comes behind the zeros
+            return true;
+            };
+            if (!(k0 + kPage > c.ctx ? rest(std::true_type{}) : rest(std::false_type{}))) break;
             __syncwarp();
             id = next;
             load(id, false);
@@ -370,8 +381,8 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         }
         const bool lost = __syncthreads_or(dead);
         if (lost) break;
-        const bool whole = c.tile == 0 && n == c.n_tiles;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (first ? 0 : 1)) * s.rows;
+        const bool whole = n == c.n_tiles;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * s.rows;
         for (int e = tid; e < s.rows * (D / 4); e += L::kThreads) {
             const int r = e / (D / 4), col = (e % (D / 4)) * 4;
             float top = -INFINITY;
@@ -423,6 +434,9 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 
 // Short contexts: a block per item, with no partials to join, where its warps have a few pages each.
 constexpr int kItemPages = 24;
+// Beginning an item (a round of loads that nothing overlaps, the warps' join) costs about as much as
+// this many pages.
+constexpr int kPad = 12;
 
 template <int D, KvFormat F>
 cudaError_t tree_mma(const void* q, const KvPages& pages, const uint64_t* masks, void* o, tree::Shape s,
@@ -464,7 +478,7 @@ bool tree_mma_supported(int rows) { return rows <= kRows; }
 cudaError_t launch_tree_mma(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
                             const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
                             float scale, void* ws, cudaStream_t st, DevCtx ctx) {
-    const tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, H / Hkv * T, 1, kPage};
+    const tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, H / Hkv * T, 1, kPage, kPad};
     auto go = [&](auto dd) {
         constexpr int D = decltype(dd)::value;
         if (f == KvFormat::Int8) return tree_mma<D, KvFormat::Int8>(q, pages, masks, o, s, ws, scale, st, ctx);

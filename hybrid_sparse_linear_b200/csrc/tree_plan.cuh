@@ -3,12 +3,13 @@
 //
 // An item is (sequence b, KV head g, row tile rt): up to RT of the G * T query rows of the group
 // against all keys of the sequence, tiles(b) = ceil((ctx_b + T) / KT) key tiles long.  Laid end to
-// end (b outermost, then g, then rt), the items form one line of W tiles, and CTA c of n takes the
-// tiles [W c / n, W (c + 1) / n): every CTA has the same number of tiles, however ragged the
-// contexts are, and no host-side knowledge of them is needed.  A CTA whose run covers an item
-// whole writes the result; else it leaves a partial (row maximum, row sum, unnormalised output)
-// in one of its two slots -- slot 0 for the item its run begins in, slot 1 for a later one -- and
-// the join kernel, which redoes the same arithmetic, adds up the partials in CTA order.
+// end (b outermost, then g, then rt), each behind `pad` empty places that stand for the cost of
+// beginning an item, the items form one line of W places, and CTA c of n takes the places
+// [W c / n, W (c + 1) / n): every CTA has about the same work, however ragged the contexts are, and
+// no host-side knowledge of them is needed.  A CTA that has all tiles of an item writes the result;
+// else it leaves a partial (row maximum, row sum, unnormalised output) in one of its two slots --
+// slot 1 when it has the item's first tile, else slot 0 -- and the join kernel, which redoes the same
+// arithmetic, adds up the partials in CTA order.
 #pragma once
 
 #include "common.cuh"
@@ -22,6 +23,7 @@ struct Shape {
     int rows;            // G * T query rows per (b, g)
     int n_rt;            // row tiles per (b, g)
     int kt;              // keys per tile
+    int pad;             // places in front of an item
 };
 
 __host__ __device__ __forceinline__ int row_tiles(int rows, int rt) { return (rows + rt - 1) / rt; }
@@ -38,17 +40,20 @@ __device__ __forceinline__ int ctx_of(const Shape& s, int b, bool* bad = nullptr
 }
 __device__ __forceinline__ int tiles_of(const Shape& s, int ctx) { return (ctx + s.T + s.kt - 1) / s.kt; }
 
+// Places of an item of sequence b.
+__device__ __forceinline__ int places_of(const Shape& s, int ctx) { return tiles_of(s, ctx) + s.pad; }
+
 // W, by one converged warp (every lane gets it).
-__device__ __forceinline__ long long total_tiles(const Shape& s, int lane, bool* bad) {
+__device__ __forceinline__ long long total_places(const Shape& s, int lane, bool* bad) {
     long long w = 0;
-    for (int b = lane; b < s.B; b += 32) w += tiles_of(s, ctx_of(s, b, bad));
+    for (int b = lane; b < s.B; b += 32) w += places_of(s, ctx_of(s, b, bad));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
     return w * s.Hkv * s.n_rt;
 }
 
 __device__ __forceinline__ long long run_start(long long w, int c, int n) { return w * c / n; }
-// The CTA whose run holds tile x (0 <= x < w).
+// The CTA whose run holds place x (0 <= x < w).
 __device__ __forceinline__ int run_of(long long w, long long x, int n) {
     return (int)(((x + 1) * n - 1) / w);  // the last c with floor(w c / n) <= x
 }
@@ -57,12 +62,12 @@ __device__ __forceinline__ int run_of(long long w, long long x, int n) {
 struct Cursor {
     int b, g, rt;
     int ctx, n_tiles;    // of sequence b
-    int tile;            // first tile of the item inside the run
-    long long left;      // tiles of the run from here on
+    int tile;            // first tile of the item inside the run (negative: that many places before it)
+    long long left;      // places of the run from here on
 };
 
-// The position of tile x of the line, by one converged warp; left is the run's length.
-__device__ __forceinline__ Cursor find_tile(const Shape& s, long long x, long long left, int lane) {
+// The cursor at place x of the line, by one converged warp; left is the run's length.
+__device__ __forceinline__ Cursor find_place(const Shape& s, long long x, long long left, int lane) {
     Cursor c;
     c.left = left;
     const long long per = (long long)s.Hkv * s.n_rt;
@@ -70,7 +75,7 @@ __device__ __forceinline__ Cursor find_tile(const Shape& s, long long x, long lo
     for (int b0 = 0; b0 < s.B; b0 += 32) {
         const int b = b0 + lane;
         const int ctx = b < s.B ? ctx_of(s, b) : 0;
-        long long n = b < s.B ? tiles_of(s, ctx) * per : 0, inc = n;
+        long long n = b < s.B ? places_of(s, ctx) * per : 0, inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long up = __shfl_up_sync(0xffffffffu, inc, o);
@@ -84,8 +89,9 @@ __device__ __forceinline__ Cursor find_tile(const Shape& s, long long x, long lo
             c.b = b0 + w;
             c.n_tiles = tiles_of(s, c.ctx);
             const long long r = x - start;
-            const int item = (int)(r / c.n_tiles);
-            c.tile = (int)(r - (long long)item * c.n_tiles);
+            const int len = c.n_tiles + s.pad;
+            const int item = (int)(r / len);
+            c.tile = (int)(r - (long long)item * len) - s.pad;
             c.g = item / s.n_rt;
             c.rt = item - c.g * s.n_rt;
             return c;
@@ -99,15 +105,20 @@ __device__ __forceinline__ Cursor find_tile(const Shape& s, long long x, long lo
     return c;
 }
 
-// Tiles of the cursor's item inside the run.
-__device__ __forceinline__ int run_tiles(const Cursor& c) {
+// Places of the cursor's item inside the run, and the tiles among them: [first_tile, first_tile + n).
+__device__ __forceinline__ int run_places(const Cursor& c) {
     const long long n = c.n_tiles - c.tile;
     return (int)(n < c.left ? n : c.left);
 }
+__device__ __forceinline__ int first_tile(const Cursor& c) { return c.tile < 0 ? 0 : c.tile; }
+__device__ __forceinline__ int run_tiles(const Cursor& c) {
+    const int n = run_places(c) + (c.tile < 0 ? c.tile : 0);
+    return n < 0 ? 0 : n;
+}
 
 __device__ __forceinline__ void next_item(const Shape& s, Cursor& c) {
-    c.left -= run_tiles(c);
-    c.tile = 0;
+    c.left -= run_places(c);
+    c.tile = -s.pad;
     if (++c.rt == s.n_rt) {
         c.rt = 0;
         if (++c.g == s.Hkv) {

@@ -2,10 +2,13 @@
 // bf16 queries; the cache in bf16 or as 8-bit codes with one scale per row.
 //
 // The G * T query rows of a KV head are its M: rows (head g, token t) are contiguous in q.  Above 128
-// rows an item takes 256 (two tiles A and B that share every K and V tile); up to 128 rows there is
-// one tile of rows, and A takes the even, B the odd key tiles of the CTA's run, each with its own
-// accumulator, joined at the end: either way two chains S -> softmax -> PV run against each other.
-// Work is divided by key tiles of 128 (tree_plan.cuh), so a single sequence uses every SM.
+// rows (wide) an item takes 256, two tiles A and B that share every K and V tile of 128 keys.  Up to
+// 128 rows (narrow) there is one tile of rows, and A takes the even, B the odd 64-key tiles of the
+// CTA's run, each with its own ring and accumulator, joined at the end.  Either way two chains
+// S -> softmax -> PV run against each other; the narrow form also has two S buffers per chain, so the
+// next S does not wait for this one's PV (its chain is short and latency counts; the wide form fills
+// its TMEM with 128-column S tiles, which feed the tensor core better).
+// Work is divided by key tiles (tree_plan.cuh), so a single sequence uses every SM.
 //
 // Bound: HBM for few rows (a key and value row are read once per 256 query rows: 4 G T d flops
 // against 4 d bytes, 2 (d + 4) in 8 bits), the tensor pipe from about T = 16 at G = 16.
@@ -38,6 +41,7 @@ using namespace ptx;
 using namespace smx;
 
 constexpr int kConvThreads = 128;
+constexpr int kPad = 3;  // beginning an item (Q, the first tiles' chain, the epilogue) costs about three tiles
 
 template <int D, KvFormat F, bool kWide>
 struct Layout {
@@ -45,28 +49,34 @@ struct Layout {
     static constexpr int kThreads = kCodes ? 512 : 384;
     static constexpr int kRegsSoft = kCodes ? 200 : 216, kRegsRest = kCodes ? 56 : 72;
     static constexpr int kRows = kWide ? 256 : 128;          // query rows per item
-    static constexpr int kBox = 128 * 128;                   // [128 rows x 64 columns] bf16, swizzled
-    static constexpr int kTile = (D / 64) * kBox;            // one Q, K or V tile
-    static constexpr int kRaw = kKeys * D;                   // the codes of one
+    static constexpr int kK = kWide ? 128 : 64;              // keys per tile
+    static constexpr int kPages = kK / kPage;
+    static constexpr int kBufs = kWide ? 1 : 2;              // S buffers per tile of rows
+    static constexpr int kQBox = 128 * 128;                  // [128 rows x 64 columns] bf16, swizzled
+    static constexpr int kQTile = (D / 64) * kQBox;
+    static constexpr int kBox = kK * 128;                    // [kK rows x 64 columns]
+    static constexpr int kTile = (D / 64) * kBox;            // a K or V tile
+    static constexpr int kRaw = kK * D;                      // the codes of one
     // K and V tiles: one ring that both tiles of rows use, or one for each.
-    static constexpr int kRing = (kWide ? (kCodes ? 3 : 5) : (kCodes ? 2 : 3)) * (128 / D);
+    static constexpr int kRing = (kWide ? (kCodes ? 3 : 5) : (kCodes ? 4 : 5)) * (128 / D);
     static constexpr int kSlots = kWide ? kRing : 2 * kRing;
-    static constexpr int kRawSlots = kCodes ? 3 * (128 / D) : 0;
+    static constexpr int kRawSlots = kCodes ? (kWide ? 3 : 6) * (128 / D) : 0;
     // The tiles first (each 1024-byte aligned), then the small parts.
-    static constexpr int kOffRing = (kWide ? 2 : 1) * kTile;
+    static constexpr int kOffRing = (kWide ? 2 : 1) * kQTile;
     static constexpr int kOffRaw = kOffRing + kSlots * kTile;
     static constexpr int kOffRawScale = kOffRaw + kRawSlots * kRaw;
-    static constexpr int kOffScale = kOffRawScale + kRawSlots * kKeys * 4;
-    static constexpr int kOffNotes = kOffScale + (kCodes ? kSlots * kKeys * 4 : 0);
+    static constexpr int kOffScale = kOffRawScale + kRawSlots * kK * 4;
+    static constexpr int kOffNotes = kOffScale + (kCodes ? kSlots * kK * 4 : 0);
     static constexpr int kNoteBytes = kCodes ? 0 : 2 * D * 8;    // sign x column, a bit per draft
-    static constexpr int kOffBars = kOffNotes + kNoteBytes;
+    static constexpr int kOffMerge = kOffNotes + kNoteBytes;     // (maximum, sum) of tile B's rows
+    static constexpr int kOffBars = kOffMerge + (kWide ? 0 : 128 * 8);
 };
 
 // An item's part in this CTA's run.
 struct Item {
     int b, g, rt, ctx;
     int tile, n;      // key tiles [tile, tile + n) (n 0: no more)
-    int first, whole;  // the run's first item; the run covers the item whole
+    int whole;         // the run has all of them
 };
 // A V tile to look through.
 struct Look {
@@ -81,7 +91,7 @@ struct Bars {
     uint64_t full[L::kSlots], empty[L::kSlots];
     uint64_t raw_full[L::kRawSlots + 1], raw_empty[L::kRawSlots + 1];
     uint64_t q_full[2], q_empty;
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // per tile and S buffer
     uint64_t v_landed[2], look_free[2];  // alternating over the looks
     uint64_t v_seen[2];                  // per item parity: its drafts' V is looked through
     uint64_t b_done, merged;             // tile B's accumulator is complete; tile A has read it
@@ -89,7 +99,7 @@ struct Bars {
     uint64_t fin[2];
     Item item[2];
     Look look[2];
-    int pages[L::kSlots];                // as Look::pages, per K tile
+    int pages[2][8];                     // as Look::pages, per ring and key tile (a ring holds at most 6)
     int raw_pages[L::kRawSlots + 1];
     int noted_it;                        // the item that the notes belong to
     uint32_t tmem_base;
@@ -106,11 +116,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     constexpr bool kCodes = L::kCodes;
     constexpr uint32_t kRing = L::kRing, kSlots = L::kSlots, kRawSlots = kCodes ? L::kRawSlots : 1;
     constexpr uint32_t kColO = 0, kColS = 256;
+    constexpr int kK = L::kK, kBufs = L::kBufs;
     extern __shared__ __align__(1024) uint8_t sm[];  // all of the block's shared memory
     Bars<L>& bars = *reinterpret_cast<Bars<L>*>(sm + L::kOffBars);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &bars.abort;
     unsigned long long* notes = reinterpret_cast<unsigned long long*>(sm + L::kOffNotes);
+    float2* merge = reinterpret_cast<float2*>(sm + L::kOffMerge);
 
     cudaTriggerProgrammaticLaunchCompletion();  // the join may be set up; it waits for this grid's end
     if (warp == 9) {
@@ -120,7 +132,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     if (tid == 0) {
         for (uint32_t i = 0; i < kSlots; ++i) {
             mbar_init(&bars.full[i], kCodes ? kConvThreads / 32 : 1);
-            mbar_init(&bars.empty[i], kWide ? 8 : 4);  // the softmax warps of the tiles that use it
+            // Handed back by the commit of the tile's MMAs that read it and, where it has scales, by the
+            // softmax warps; by both tiles of rows where they share it.
+            mbar_init(&bars.empty[i], (kWide ? 2 : 1) * (kCodes ? 5 : 1));
         }
         for (uint32_t i = 0; i < kRawSlots; ++i) {
             mbar_init(&bars.raw_full[i], 1);
@@ -128,9 +142,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bars.q_full[x], 1);
-            mbar_init(&bars.s_full[x], 1);
-            mbar_init(&bars.p_full[x], 4);
-            mbar_init(&bars.o_full[x], 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&bars.s_full[x][j], 1);
+                mbar_init(&bars.p_full[x][j], 4);
+                mbar_init(&bars.pv_done[x][j], 1);
+            }
             mbar_init(&bars.v_landed[x], 1);
             mbar_init(&bars.look_free[x], 1);
             mbar_init(&bars.v_seen[x], 1);
@@ -178,18 +194,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (warp == 8) {
             // ------------------------------------------------------------ items and loads
             bool bad = false;
-            const long long w = tree::total_tiles(s, lane, &bad);
+            const long long w = tree::total_places(s, lane, &bad);
             if (bad && blockIdx.x == 0) flag(ctx, kStatusBounds);
             const long long x0 = tree::run_start(w, blockIdx.x, gridDim.x);
-            tree::Cursor c = tree::find_tile(s, x0, tree::run_start(w, blockIdx.x + 1, gridDim.x) - x0, lane);
+            tree::Cursor c = tree::find_place(s, x0, tree::run_start(w, blockIdx.x + 1, gridDim.x) - x0, lane);
             uint32_t rc[2] = {0, 0}, rr = 0, kq = 0, looks = 0;  // entries, raw tiles, Q tiles, looks
             uint32_t via = 0;  // slots whose last load went to v_landed
             bool ok = true;
             for (int it = 0; ok; ++it) {
-                const int n = tree::run_tiles(c);
+                while (c.left > 0 && tree::run_tiles(c) == 0) tree::next_item(s, c);
+                const int n = c.left > 0 ? tree::run_tiles(c) : 0, t0 = tree::first_tile(c);
                 if (it >= 2 && !wait_warp(&bars.item_empty[it & 1], ((it - 2) >> 1) & 1, ctx, abort)) break;
                 if (lane == 0) {
-                    bars.item[it & 1] = Item{c.b, c.g, c.rt, c.ctx, c.tile, n, it == 0, n == c.n_tiles};
+                    bars.item[it & 1] = Item{c.b, c.g, c.rt, c.ctx, t0, n, n == c.n_tiles};
                     mbar_arrive(&bars.item_full[it & 1]);
                 }
                 if (n == 0) break;
@@ -197,28 +214,29 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 if (lane == 0) {
                     const int y = (c.b * s.Hkv + c.g) * s.rows + c.rt * L::kRows;
                     for (int x = 0; x < (kWide ? 2 : 1); ++x) {
-                        mbar_arrive_expect_tx(&bars.q_full[x], L::kTile);
+                        mbar_arrive_expect_tx(&bars.q_full[x], L::kQTile);
                         for (int h = 0; h < D / 64; ++h)
-                            tma_load_2d(sm + x * L::kTile + h * L::kBox, &tmQ, &bars.q_full[x], 64 * h, y + 128 * x);
+                            tma_load_2d(sm + x * L::kQTile + h * L::kQBox, &tmQ, &bars.q_full[x], 64 * h, y + 128 * x);
                     }
                 }
                 ++kq;
                 const int keys = c.ctx + s.T;
                 int ids = -1;
                 for (int i = 0; ok && i < n; ++i) {
-                    const int t = c.tile + i;
-                    if ((i & 15) == 0) ids = page_of(pages, c.b, 2 * t + lane);  // of 16 key tiles
-                    int id[2];
+                    const int t = t0 + i;
+                    constexpr int kP = L::kPages, kBatch = 32 / kP;  // key tiles that 32 pages make
+                    if (i % kBatch == 0) ids = page_of(pages, c.b, kP * t + lane);
+                    int id[2] = {0, 0};
                     int have = 0;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        id[h] = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + h);
-                        if (t * kKeys + h * kPage < keys) {
+                    for (int h = 0; h < kP; ++h) {
+                        id[h] = __shfl_sync(0xffffffffu, ids, kP * (i % kBatch) + h);
+                        if (t * kK + h * kPage < keys) {
                             if (id[h] >= 0) have |= 1 << h;
                             else if (lane == 0) flag(ctx, kStatusBounds);  // left out
                         }
                     }
-                    const bool drafts = (t + 1) * kKeys > c.ctx;  // keys that some row does not see
+                    const bool drafts = (t + 1) * kK > c.ctx;  // keys that some row does not see
                     for (int j = 0; ok && j < 2; ++j) {  // K, V
                         const int row[2] = {(id[0] * s.Hkv + c.g) * kPage, (id[1] * s.Hkv + c.g) * kPage};
                         if constexpr (kCodes) {
@@ -231,11 +249,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                                 mbar_arrive_expect_tx(&bars.raw_full[q], __popc(have) * (kPage * D + kPage * 4));
                                 const uint8_t* codes = static_cast<const uint8_t*>(j ? pages.v : pages.k);
                                 const float* scales = j ? pages.v_scale : pages.k_scale;
-                                for (int h = 0; h < 2; ++h)
+                                for (int h = 0; h < kP; ++h)
                                     if ((have >> h) & 1) {
                                         bulk_load_g2s(sm + L::kOffRaw + q * L::kRaw + h * kPage * D,
                                                       codes + (int64_t)row[h] * D, kPage * D, &bars.raw_full[q]);
-                                        bulk_load_g2s(sm + L::kOffRawScale + (q * kKeys + h * kPage) * 4,
+                                        bulk_load_g2s(sm + L::kOffRawScale + (q * kK + h * kPage) * 4,
                                                       scales + row[h], kPage * 4, &bars.raw_full[q]);
                                     }
                             }
@@ -244,19 +262,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                             const uint32_t e = odd ? rc[1] : rc[0], q = slot_of(odd, e);
                             if (e >= kRing && !(ok = wait_warp(&bars.empty[q], use_of(e - kRing), ctx, abort)))
                                 break;
-                            const bool look = j == 1 && (drafts || have != 3);
+                            const bool look = j == 1 && (drafts || have != (1 << kP) - 1);
                             if (look && looks >= 2 &&
                                 !(ok = wait_warp(&bars.look_free[looks & 1], ((looks - 2) >> 1) & 1, ctx, abort)))
                                 break;
                             if (lane == 0) {
                                 uint64_t* fb = look ? &bars.v_landed[looks & 1] : &bars.full[q];
-                                if (j == 0) bars.pages[q] = have;
-                                if (look) bars.look[looks & 1] = Look{(int)q, t * kKeys, c.ctx, have, it, drafts && i == n - 1};
-                                mbar_arrive_expect_tx(fb, __popc(have) * (L::kTile / 2));
-                                for (int h = 0; h < 2; ++h)
+                                if (j == 0) bars.pages[odd][(e >> 1) & 7] = have;
+                                if (look) bars.look[looks & 1] = Look{(int)q, t * kK, c.ctx, have, it, drafts && i == n - 1};
+                                mbar_arrive_expect_tx(fb, __popc(have) * (L::kTile / kP));
+                                for (int h = 0; h < kP; ++h)
                                     if ((have >> h) & 1)
                                         for (int p = 0; p < D / 64; ++p)
-                                            tma_load_2d(slot_ptr(q) + p * L::kBox + h * (L::kBox / 2),
+                                            tma_load_2d(slot_ptr(q) + p * L::kBox + h * (L::kBox / kP),
                                                         j ? &tmV : &tmK, fb, 64 * p, row[h]);
                             }
                             via = (via & ~(1u << q)) | ((look ? 1u : 0u) << q);
@@ -293,49 +311,55 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
         } else if (warp < 11) {
             // ------------------------------------------------------------ MMA issuers
-            // As in the packed kernel: S of the tile's next key tile right behind PV of this one.
+            // Order per tile: PV of a key tile, then S of the one kBufs further, which lies over the P
+            // that this PV read; MMAs of one thread run in order.  The whole warp runs the loop and one
+            // elected lane issues.
             const int x = warp - 9;
             auto wait_w = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, ctx, abort); };
             const uint32_t dO = tmem + kColO + x * 128, dS = tmem + kColS + x * 128;
             const uint64_t dhi = (uint64_t)sdesc_sw128_hi(1024) << 32;
-            const uint64_t q_d = dhi | sdesc_sw128_lo(smem_u32(sm + (kWide ? x : 0) * L::kTile), 16);
+            const uint64_t q_d = dhi | sdesc_sw128_lo(smem_u32(sm + (kWide ? x : 0) * L::kQTile), 16);
             const uint64_t k_d0 = dhi | sdesc_sw128_lo(smem_u32(sm + L::kOffRing), 16);
             const uint64_t v_d0 = dhi | sdesc_sw128_lo(smem_u32(sm + L::kOffRing), L::kBox);
-            constexpr uint32_t idS = idesc_bf16_f32(128, kKeys, false, false);
+            constexpr uint32_t idS = idesc_bf16_f32(128, kK, false, false);
             constexpr uint32_t idPV = idesc_bf16_f32(128, D, false, true);
-            uint32_t rc = 0, np = 0;
+            uint32_t rc = 0, a = 0;  // ring entries, key tiles of the items before
             bool ok = true;
             Item m;
             for (int it = 0; ok && take_item(it, m); ++it) {
                 const int nx = my_tiles(m.n, x);
                 auto issue_s = [&](int k) -> bool {
-                    const uint32_t e = rc + 2 * k, q = slot_of(x, e);
+                    const uint32_t e = rc + 2 * k, q = slot_of(x, e), j = (a + k) % kBufs;
                     if (!wait_w(&bars.full[q], use_of(e))) return false;
                     tc_fence_after();
                     const uint64_t k_d = k_d0 + q * (L::kTile >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * L::kBox + (ks & 3) * 32) >> 4;
-                        mma_ss_elect(dS, q_d + off, k_d + off, idS, ks > 0 ? 1u : 0u);
-                    }
-                    mma_commit_elect(&bars.s_full[x]);
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_ss_elect(dS + j * 64, q_d + (((ks >> 2) * L::kQBox + (ks & 3) * 32) >> 4),
+                                     k_d + (((ks >> 2) * L::kBox + (ks & 3) * 32) >> 4), idS, ks > 0 ? 1u : 0u);
+                    mma_commit_elect(&bars.s_full[x][j]);
+                    mma_commit_elect(&bars.empty[q]);
                     return true;
                 };
-                ok = wait_w(&bars.q_full[kWide ? x : 0], it & 1) && (nx == 0 || issue_s(0));
+                ok = wait_w(&bars.q_full[kWide ? x : 0], it & 1);
+                for (int k = 0; ok && k < kBufs && k < nx; ++k) ok = issue_s(k);
                 for (int k = 0; ok && k < nx; ++k) {
-                    const uint32_t e = rc + 2 * k + 1, q = slot_of(x, e);
-                    ok = wait_w(&bars.p_full[x], np++ & 1) && wait_w(&bars.full[q], use_of(e));
+                    const uint32_t e = rc + 2 * k + 1, q = slot_of(x, e), j = (a + k) % kBufs;
+                    ok = wait_w(&bars.p_full[x][j], ((a + k) / kBufs) & 1) && wait_w(&bars.full[q], use_of(e));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t v_d = v_d0 + q * (L::kTile >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)
-                        mma_ts_elect(dO, dS + ks * 8, v_d + ((ks * 16 * 128) >> 4), idPV, (k > 0 || ks > 0) ? 1u : 0u);
-                    if (k + 1 < nx) ok = issue_s(k + 1);
+                    for (int ks = 0; ks < kK / 16; ++ks)
+                        mma_ts_elect(dO, dS + j * 64 + ks * 8, v_d + ((ks * 16 * 128) >> 4), idPV,
+                                     (k > 0 || ks > 0) ? 1u : 0u);
+                    mma_commit_elect(&bars.pv_done[x][j]);
+                    mma_commit_elect(&bars.empty[q]);
+                    if (k + kBufs < nx) ok = issue_s(k + kBufs);
                 }
                 rc += 2 * nx;
+                a += nx;
                 if (ok) mma_commit_elect(&bars.q_empty);  // every S that reads this item's Q is done
-                if (ok && nx > 0) mma_commit_elect(&bars.o_full[x]);
                 leave_item(it);
             }
             mma_commit_elect(&bars.fin[x]);
@@ -351,7 +375,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     constexpr int kC = D / 8;  // 16-byte pieces per row
                     uint8_t* tile = slot_ptr(v.slot);
                     const int keys = v.ctx + s.T;
-                    for (int c0 = 0; c0 < kKeys * kC; c0 += 32) {
+                    for (int c0 = 0; c0 < kK * kC; c0 += 32) {
                         const int r = (c0 + lane) / kC, c = (c0 + lane) % kC, j = v.k0 + r - v.ctx;
                         uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * L::kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
                         bool bad = false;
@@ -409,21 +433,34 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         uint8_t* tile = slot_ptr(q);
                         // A lane takes 16 codes, four lanes 64 columns of a row, neighbouring rows the
                         // other 64: eight lanes then read and (through the swizzle) write all 32 banks.
-                        constexpr int kC = D / 16;
-#pragma unroll 4
-                        for (int e = ct; e < kKeys * kC; e += kConvThreads) {
-                            const int r = (e >> 2) % kKeys, c = e & 3;
-                            const int box = D == 64 ? 0 : (r + e / (kKeys * 4)) & 1;
-                            const uint4 u = *reinterpret_cast<const uint4*>(raw + r * D + box * 64 + c * 16);
-                            uint8_t* row = tile + box * L::kBox + r * 128;
-                            const uint2 a0 = codes_to_bf16<F>(u.x), a1 = codes_to_bf16<F>(u.y);
-                            const uint2 a2 = codes_to_bf16<F>(u.z), a3 = codes_to_bf16<F>(u.w);
-                            *reinterpret_cast<uint4*>(row + (((2 * c) ^ (r & 7)) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-                            *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (r & 7)) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
+                        constexpr int kN = kK * (D / 16) / kConvThreads;  // pieces of 16 codes per thread
+                        constexpr int kB = kN < 4 ? kN : 4;
+#pragma unroll
+                        for (int b0 = 0; b0 < kN; b0 += kB) {
+                            uint4 u[kB];  // read before the first write, which the compiler keeps in order
+#pragma unroll
+                            for (int b = 0; b < kB; ++b) {
+                                const int e = ct + (b0 + b) * kConvThreads, r = (e >> 2) % kK;
+                                const int box = D == 64 ? 0 : (r + e / (kK * 4)) & 1;
+                                u[b] = *reinterpret_cast<const uint4*>(raw + r * D + box * 64 + (e & 3) * 16);
+                            }
+#pragma unroll
+                            for (int b = 0; b < kB; ++b) {
+                                const int e = ct + (b0 + b) * kConvThreads, r = (e >> 2) % kK, c = e & 3;
+                                const int box = D == 64 ? 0 : (r + e / (kK * 4)) & 1;
+                                uint8_t* row = tile + box * L::kBox + r * 128;
+                                const uint2 a0 = codes_to_bf16<F>(u[b].x), a1 = codes_to_bf16<F>(u[b].y);
+                                const uint2 a2 = codes_to_bf16<F>(u[b].z), a3 = codes_to_bf16<F>(u[b].w);
+                                *reinterpret_cast<uint4*>(row + (((2 * c) ^ (r & 7)) << 4)) =
+                                    make_uint4(a0.x, a0.y, a1.x, a1.y);
+                                *reinterpret_cast<uint4*>(row + (((2 * c + 1) ^ (r & 7)) << 4)) =
+                                    make_uint4(a2.x, a2.y, a3.x, a3.y);
+                            }
                         }
-                        reinterpret_cast<float*>(sm + L::kOffScale)[q * kKeys + ct] =
-                            reinterpret_cast<const float*>(sm + L::kOffRawScale)[raw_of(rr) * kKeys + ct];
-                        if (ct == 0) bars.pages[q] = bars.raw_pages[raw_of(rr)];
+                        if (ct < kK)
+                            reinterpret_cast<float*>(sm + L::kOffScale)[q * kK + ct] =
+                                reinterpret_cast<const float*>(sm + L::kOffRawScale)[raw_of(rr) * kK + ct];
+                        if (ct == 0 && !(i & 1)) bars.pages[odd][(e2 >> 1) & 7] = bars.raw_pages[raw_of(rr)];
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -443,11 +480,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const uint32_t lane_base = tmem_lane_base(warp);
         const uint32_t colO = tmem + lane_base + kColO + x * 128;
         const uint32_t colS = tmem + lane_base + kColS + x * 128;
-        uint32_t rc = 0, rb = 0;  // entries of the tile's ring; of tile B's
-        uint32_t ns = 0, no = 0, n_two = 0, nseen[2] = {0, 0};
+        uint32_t rc = 0, a = 0;  // ring entries, key tiles of the items before
+        uint32_t n_two = 0, nseen[2] = {0, 0};
         bool ok = true;
-        auto give = [&](uint32_t slot) {  // this warp is done with what is there
-            if (lane == 0) mbar_arrive(&bars.empty[slot]);
+        auto give = [&](uint32_t slot) {  // this warp has read the scales there
+            if (kCodes && lane == 0) mbar_arrive(&bars.empty[slot]);
         };
         Item m;
         for (int it = 0; ok && take_item(it, m); ++it) {
@@ -457,53 +494,54 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             const uint64_t bits = real ? tree::draft_bits(masks, m.b, row % s.T, s.T) : 0ull;
             const bool any_real = __any_sync(0xffffffffu, real);  // else the warp only passes stages on
             RowState st;
-            for (int k = 0; k < nx; ++k, ++ns) {
-                const int i = nth_tile(k, x), k0 = (m.tile + i) * kKeys;
-                const uint32_t e = rc + 2 * k, qk = slot_of(x, e), qv = slot_of(x, e + 1);
-                ok = wait_warp(&bars.s_full[x], ns & 1, ctx, abort) &&
-                     wait_warp(&bars.full[qk], use_of(e), ctx, abort);  // (done: for its pages, scales)
+            for (int k = 0; k < nx; ++k) {
+                const int i = nth_tile(k, x), k0 = (m.tile + i) * kK;
+                const uint32_t e = rc + 2 * k, qk = slot_of(x, e), qv = slot_of(x, e + 1), j = (a + k) % kBufs;
+                const uint32_t col = colS + j * 64;
+                ok = wait_warp(&bars.s_full[x][j], ((a + k) / kBufs) & 1, ctx, abort);
+                if (kCodes && ok) ok = wait_warp(&bars.full[qk], use_of(e), ctx, abort);  // (done: for its scales)
                 if (!ok) break;
                 tc_fence_after();
-                // PV of the tile before is done (S was committed behind it).  Its V goes back before this
-                // tile's is waited for below: they may share the slot.
-                if (k > 0) give(slot_of(x, e - 1));
                 float alpha = 1.f;
                 if (any_real) {
-                    uint32_t sr[kKeys];
+                    uint32_t sr[kK];
                     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(colS + 32 * c, chunk(sr, c));
-                    const int have = bars.pages[qk];
+                    for (int c = 0; c < kK / 32; ++c) tmem_ld32(col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
+                    const int have = bars.pages[ring_of(x)][(e >> 1) & 7];
                     tmem_ld_wait();
                     if constexpr (kCodes) {
-                        const float* ks = reinterpret_cast<const float*>(sm + L::kOffScale) + qk * kKeys;
+                        const float* ks = reinterpret_cast<const float*>(sm + L::kOffScale) + qk * kK;
 #pragma unroll
-                        for (int c = 0; c < kKeys; c += 4) {
+                        for (int c = 0; c < kK; c += 4) {
                             const float4 f = *reinterpret_cast<const float4*>(ks + c);
                             sr[c] = __float_as_uint(__uint_as_float(sr[c]) * f.x);
                             sr[c + 1] = __float_as_uint(__uint_as_float(sr[c + 1]) * f.y);
                             sr[c + 2] = __float_as_uint(__uint_as_float(sr[c + 2]) * f.z);
                             sr[c + 3] = __float_as_uint(__uint_as_float(sr[c + 3]) * f.w);
                         }
+                        __syncwarp();
+                        give(qk);
                     }
-                    const float* vs = reinterpret_cast<const float*>(sm + L::kOffScale) + qv * kKeys;
-                    if (k0 + kKeys <= m.ctx && have == 3) {
-                        const float mx = max2n(max2n(max32(sr), max32(sr + 32)), max2n(max32(sr + 64), max32(sr + 96)));
+                    const float* vs = reinterpret_cast<const float*>(sm + L::kOffScale) + qv * kK;
+                    if (k0 + kK <= m.ctx && have == (1 << L::kPages) - 1) {
+                        float mx = max32(sr);
+#pragma unroll
+                        for (int c = 1; c < kK / 32; ++c) mx = max2n(mx, max32(sr + 32 * c));
                         alpha = st.raise(mx * sl2);
                         const float nb = st.shift();
-                        // The scales of V's rows are there once V is (the softmax of codes waits for it).
-                        if (kCodes) ok = wait_warp(&bars.full[qv], use_of(e + 1), ctx, abort);
+                        if (kCodes) ok = wait_warp(&bars.full[qv], use_of(e + 1), ctx, abort);  // V's scales
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < kK / 32; ++c) {
                             uint32_t pk[16];
                             exp32<false, kCodes>(sr + 32 * c, sl2, nb, 0u, vs + 32 * c, acc, pk);
-                            tmem_st16(colS + 16 * c, pk);
+                            tmem_st16(col + 16 * c, pk);
                         }
                     } else {
-                        uint32_t seen[4];
+                        uint32_t seen[kK / 32];
                         float mx = -INFINITY;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < kK / 32; ++c) {
                             const int d0 = k0 + 32 * c - m.ctx;  // draft number of the chunk's first key
                             const uint32_t drafts = d0 >= 64 ? 0u : d0 >= 0 ? (uint32_t)(bits >> d0)
                                                   : d0 > -32 ? (uint32_t)(bits << -d0) : 0u;
@@ -514,61 +552,64 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         const float nb = st.shift();
                         if (kCodes) ok = wait_warp(&bars.full[qv], use_of(e + 1), ctx, abort);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < kK / 32; ++c) {
                             uint32_t pk[16];
                             exp32<true, kCodes>(sr + 32 * c, sl2, nb, seen[c], vs + 32 * c, acc, pk);
-                            tmem_st16(colS + 16 * c, pk);
+                            tmem_st16(col + 16 * c, pk);
                         }
                     }
                     st.l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+                } else {
+                    give(qk);
+                    if (kCodes) ok = wait_warp(&bars.full[qv], use_of(e + 1), ctx, abort);
                 }
                 __syncwarp();
-                give(qk);  // S is done with K, and this warp with its scales
+                give(qv);
                 if (!ok) break;
                 // Tile A reads tile B's accumulator at an item's end: B writes P, which lets the issuer
                 // start on it, only after that.
-                if (!kWide && x == 1 && k == 0 && no > 0) ok = wait_warp(&bars.merged, (no - 1) & 1, ctx, abort);
+                if (!kWide && x == 1 && k == 0 && n_two > 0) ok = wait_warp(&bars.merged, (n_two - 1) & 1, ctx, abort);
+                if (ok && k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    const uint32_t b = a + k - 1;  // the PV before has to be done with O
+                    ok = wait_warp(&bars.pv_done[x][b % kBufs], (b / kBufs) & 1, ctx, abort);
+                    if (ok) {
+                        tc_fence_after();
+                        scale_row<D>(colO, alpha);
+                    }
+                }
                 if (!ok) break;
-                if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) scale_row<D>(colO, alpha);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[x]);
+                if (lane == 0) mbar_arrive(&bars.p_full[x][j]);
             }
             if (!ok) break;
             // The drafts' V of this item is looked through (its notes can be read).
             bool noted = false;
             if constexpr (!kCodes) {
-                if ((m.tile + m.n) * kKeys > m.ctx) {
+                if ((m.tile + m.n) * kK > m.ctx) {
                     ok = wait_warp(&bars.v_seen[it & 1], nseen[it & 1]++ & 1, ctx, abort);
                     if (!ok) break;
                     noted = *reinterpret_cast<volatile int*>(&bars.noted_it) == it;
                 }
             }
-            // Tile B's maxima and sums go to tile A through B's last V tile, which A hands back.
-            float2* merge = nullptr;
+            rc += 2 * nx;
+            a += nx;
             if (nx > 0) {
-                ok = wait_warp(&bars.o_full[x], no & 1, ctx, abort);
+                ok = wait_warp(&bars.pv_done[x][(a - 1) % kBufs], ((a - 1) / kBufs) & 1, ctx, abort);
                 if (!ok) break;
                 tc_fence_after();
-                ++no;
-                rc += 2 * nx;
-                if (kWide || x == 0) give(slot_of(x, rc - 1));
             }
-            if (!kWide) {
-                rb += 2 * my_tiles(m.n, 1);
-                merge = reinterpret_cast<float2*>(slot_ptr(slot_of(1, rb - 1)));
-                if (x == 1) {
-                    if (nx > 0) {
-                        merge[r] = make_float2(st.m, st.l);
-                        fence_proxy_async_smem();  // the next tile's copy comes behind it
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars.b_done);
-                    }
-                    leave_item(it);
-                    continue;
+            if (!kWide && x == 1) {  // tile A takes it from here
+                if (nx > 0) {
+                    ++n_two;
+                    merge[r] = make_float2(st.m, st.l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars.b_done);
                 }
+                leave_item(it);
+                continue;
             }
             const bool two = !kWide && m.n > 1;
             float top = st.m, l = st.l, w_a = 1.f, w_b = 0.f;
@@ -581,13 +622,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 w_a = st.m == -INFINITY ? 0.f : ex2(st.m - top);
                 w_b = o.x == -INFINITY ? 0.f : ex2(o.x - top);
                 l = st.l * w_a + o.y * w_b;
-                __syncwarp();
-                give(slot_of(1, rb - 1));
             }
             const float inv = !m.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
             const int64_t orow = ((int64_t)m.b * s.Hkv + m.g) * s.rows + row;
             const int rt = kWide ? L::kRows : s.rows;  // rows a partial slot holds
-            const size_t slot = ((size_t)blockIdx.x * 2 + (m.first ? 0 : 1)) * rt + (kWide ? r + 128 * x : r);
+            const size_t slot = ((size_t)blockIdx.x * 2 + (m.tile > 0 ? 0 : 1)) * rt + (kWide ? r + 128 * x : r);
             if (real && !m.whole) part.ml[slot] = make_float2(top, l);
             if (any_real) {
 #pragma unroll 1
@@ -666,8 +705,9 @@ cudaError_t tree_tc(const void* q, const KvPages& pages, const uint64_t* masks, 
     constexpr int bytes = L::kOffBars + (int)sizeof(Bars<L>);
     if (cudaError_t e = ensure_smem<tree_tc_kernel<D, F, kWide>>(bytes); e != cudaSuccess) return e;
     s.n_rt = kWide ? tree::row_tiles(s.rows, L::kRows) : 1;
-    s.kt = kKeys;
-    const int tiles = (s.max_ctx + s.T + kKeys - 1) / kKeys;
+    s.kt = L::kK;
+    s.pad = kPad;
+    const int tiles = (s.max_ctx + s.T + L::kK - 1) / L::kK;
     const long long most = (long long)s.B * s.Hkv * s.n_rt * tiles;
     const int sms = device_sm_count();
     const int n_cta = most < sms ? (int)most : sms;
@@ -690,7 +730,7 @@ size_t tree_tc_workspace(int rows, int d) {
 cudaError_t launch_tree_tc(KvFormat f, const void* q, const KvPages& pages, const uint64_t* masks, void* o,
                            const int32_t* ctx_len, int max_ctx, int B, int H, int Hkv, int T, int d,
                            float scale, void* ws, cudaStream_t st, DevCtx ctx) {
-    const tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, H / Hkv * T, 0, 0};
+    const tree::Shape s{ctx_len, B, Hkv, H / Hkv, T, max_ctx, H / Hkv * T, 0, 0, 0};
     auto go = [&](auto dd, auto ff) {
         constexpr int D = decltype(dd)::value;
         constexpr KvFormat F = decltype(ff)::value;
