@@ -3,15 +3,17 @@
 // Work unit: two tiles A and B of 128 query rows that share one KV head.  A tile packs TG query
 // heads of the head's group (the largest power of two dividing the group size, at most 16) by
 // TQ = 128 / TG consecutive tokens, so with 16 heads per KV head a unit is 16 tokens and its
-// causal edge wastes at most 15 keys per row.  A unit walks its sequence's keys in tiles of 128;
-// K and V of a tile are loaded once for both.
+// causal edge wastes at most 15 keys per row.  A unit walks its sequence's keys in tiles of 64; K and
+// V of a tile are loaded once for both.
 //
-// Per key tile and query tile X:  S_X = Q_X K^T (M128 N128),  P_X = online softmax (softmax_tile.cuh),
-// O_X += P_X V (A = P_X from TMEM over S_X's columns).  N = 128 keys is what the tensor core needs
-// to be fed: a K step then reads 8 KB from shared memory in 64 cycles, its full 128 B per cycle;
-// 64 keys would read 6 KB in 32.  TMEM: O_A, O_B, S_A, S_B, 128 columns each.  The two tiles' chains
-// S -> softmax -> PV run against each other: while one tile's softmax works, the tensor core has the
-// other's products.
+// Per key tile and query tile X:  S_X = Q_X K^T (M128 N64),  P_X = online softmax (softmax_tile.cuh),
+// O_X += P_X V (A = P_X from TMEM over S_X's columns).  TMEM: O_A, O_B (128 columns each) and two S
+// buffers of 64 columns per tile: the S of the next key tile is formed while the softmax works on this
+// one, so a tile's chain is its softmax alone, and the two tiles' chains run beside each other.  One
+// S of 128 keys per tile instead would feed the tensor core better (an N = 64 step reads 6 KB of
+// shared memory in the 32 cycles of its math, 48 at 128 B per cycle) but leaves S -> softmax -> PV in
+// line: per 128 keys it took 3900 cycles of which the tensor core worked 2048 (1008 TFLOP/s at 32768
+// tokens; two threads per row in that form, which have to meet for the row's maximum, 814).
 //
 // Only the last key tile(s) hold keys that some row must not see.  There S and PV stop at the last
 // 16-key step a row sees, rows mask by their own position, and, since a probability of zero still
@@ -21,9 +23,10 @@
 //
 // Roles (384 threads, persistent, one CTA per SM): warps 0-3 softmax and epilogue of tile A, 4-7 of
 // tile B (thread = row); warp 8 finds the units and issues the TMA loads; warps 9 and 10 issue the
-// MMAs of tiles A and B; warp 11 looks through V.  Completions: an S commit also says that the
-// tile's PV before it is done (one commit per round), and the softmax hands K and V stages back when
-// it sees one.  Every wait is bounded; a timeout sets the status word and all roles wind down.
+// MMAs of tiles A and B; warp 11 looks through V.  Completions: the issuer commits once per round,
+// after PV(k) and S(k + 2), so the commit of round k + 2 says that both are done; two more rounds
+// without an S close a unit.  The softmax hands K and V stages back as it sees the commits.  Every
+// wait is bounded; a timeout sets the status word and all roles wind down.
 #include <climits>
 
 #include "kv_format.cuh"
@@ -37,14 +40,17 @@ using namespace ptx;
 using namespace smx;
 
 constexpr int kThreads = 384;
+constexpr int kK = 64;   // keys per tile
 constexpr int kConsumerWarps = 11;  // all but the unit finder
 
 template <int D>
 struct Layout {
-    static constexpr int kBox = 128 * 128;            // [128 rows x 64 columns] bf16, 128-byte swizzle
-    static constexpr int kTile = (D / 64) * kBox;     // one Q, K or V tile
-    static constexpr int kSlots = D == 128 ? 5 : 8;   // ring of K and V tiles
-    static constexpr int kOffRing = 2 * kTile;
+    static constexpr int kQBox = 128 * 128;           // [128 rows x 64 columns] bf16, 128-byte swizzle
+    static constexpr int kQTile = (D / 64) * kQBox;
+    static constexpr int kBox = kK * 128;             // [kK rows x 64 columns]
+    static constexpr int kTile = (D / 64) * kBox;     // a K or V tile
+    static constexpr int kSlots = 10;                 // ring of K and V tiles
+    static constexpr int kOffRing = 2 * kQTile;
     static constexpr int kOffNotes = kOffRing + kSlots * kTile;
     static constexpr int kNoteBytes = 2 * 2 * D * 2;  // unit parity x sign x column, uint16
     static constexpr int kBytes = kOffNotes + kNoteBytes + 1024;  // + alignment of the base
@@ -59,8 +65,8 @@ template <int kSlots>
 struct Bars {
     uint64_t full[kSlots], empty[kSlots];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2];
-    uint64_t v_landed[2][2];  // V tiles to look through, per unit parity (at most two a unit)
+    uint64_t s_full[2][2], p_full[2][2];  // per tile, alternating over the rounds
+    uint64_t v_landed[2][4];  // V tiles to look through, per unit parity (at most four a unit)
     uint64_t v_seen[2];       // per unit parity: warp 11 is through with the unit
     uint64_t unit_full[2], unit_empty[2];
     uint64_t fin[2];
@@ -80,8 +86,8 @@ __device__ __forceinline__ int key_tiles(const Unit& u, int x, int tq, int* last
         return 0;
     }
     const int last = min(t0 + tq, u.len) - 1;  // last token, the last key its rows see
-    *last_keys = ((last % kKeys) / 16 + 1) * 16;
-    return last / kKeys + 1;
+    *last_keys = ((last % kK) / 16 + 1) * 16;
+    return last / kK + 1;
 }
 
 template <int D>
@@ -113,17 +119,17 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bars.q_full[x], 1);
             mbar_init(&bars.q_empty[x], 1);
-            mbar_init(&bars.s_full[x], 1);
-            mbar_init(&bars.p_full[x], 4);
-            mbar_init(&bars.o_full[x], 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&bars.s_full[x][j], 1);
+                mbar_init(&bars.p_full[x][j], 4);
+            }
             mbar_init(&bars.unit_full[x], 1);
             mbar_init(&bars.unit_empty[x], kConsumerWarps);
             mbar_init(&bars.fin[x], 1);
             bars.noted[x] = 0;
         }
         for (int j = 0; j < 2; ++j) {
-            mbar_init(&bars.v_landed[j][0], 1);
-            mbar_init(&bars.v_landed[j][1], 1);
+            for (int i = 0; i < 4; ++i) mbar_init(&bars.v_landed[j][i], 1);
             mbar_init(&bars.v_seen[j], 1);
         }
         bars.abort = 0;
@@ -155,7 +161,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (warp == 8) {
             // ------------------------------------------------------------ units and loads
             uint32_t rc = 0, kq[2] = {0, 0};
-            uint32_t nl[2][2] = {{0, 0}, {0, 0}};  // uses of v_landed
+            uint32_t nl[2][4] = {};  // uses of v_landed
             uint32_t via = 0;                      // slots whose last load went to v_landed
             for (int it = 0;; ++it) {
                 // Every other round runs the CTAs backwards: units come longest first within a
@@ -182,9 +188,9 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                             stop = 1;
                             return;
                         }
-                        mbar_arrive_expect_tx(&bars.q_full[x], L::kTile);
+                        mbar_arrive_expect_tx(&bars.q_full[x], L::kQTile);
                         for (int h = 0; h < D / 64; ++h)
-                            tma_load_3d(sm + x * L::kTile + h * L::kBox, &tmQ, &bars.q_full[x], 64 * h,
+                            tma_load_3d(sm + x * L::kQTile + h * L::kQBox, &tmQ, &bars.q_full[x], 64 * h,
                                         u.start + u.first + x * tq, u.hg * tg);
                         ++kq[x];
                     };
@@ -196,14 +202,14 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                             break;
                         }
                         // A V tile that warp 11 looks through lands there; the warp then passes it on.
-                        const int look = (e & 1) ? (e >> 1) - u.first / kKeys : -1;
+                        const int look = (e & 1) ? (e >> 1) - u.first / kK : -1;
                         uint64_t* fb = look >= 0 ? &bars.v_landed[it & 1][look] : &bars.full[slot_of(rc)];
                         if (look >= 0) ++nl[it & 1][look];
                         via = (via & ~(1u << slot_of(rc))) | ((look >= 0 ? 1u : 0u) << slot_of(rc));
                         mbar_arrive_expect_tx(fb, L::kTile);
                         for (int h = 0; h < D / 64; ++h)
                             tma_load_3d(slot_ptr(rc) + h * L::kBox, (e & 1) ? &tmV : &tmK, fb, 64 * h,
-                                        u.start + (e >> 1) * kKeys, kvh);
+                                        u.start + (e >> 1) * kK, kvh);
                         if (e == 0) load_q(1);
                     }
                 }
@@ -213,70 +219,71 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (lane == 0) {  // drain: every copy this warp started has landed before the block exits
                 for (int x = 0; x < 2; ++x)
                     if (kq[x] > 0) (void)mbar_wait(&bars.q_full[x], (kq[x] - 1) & 1, ctx);
-                for (int j = 0; j < 4; ++j)
-                    if (nl[j >> 1][j & 1] > 0)
-                        (void)mbar_wait(&bars.v_landed[j >> 1][j & 1], (nl[j >> 1][j & 1] - 1) & 1, ctx);
+                for (int j = 0; j < 8; ++j)
+                    if (nl[j >> 2][j & 3] > 0)
+                        (void)mbar_wait(&bars.v_landed[j >> 2][j & 3], (nl[j >> 2][j & 3] - 1) & 1, ctx);
                 for (uint32_t e = rc > kSlots ? rc - kSlots : 0; e < rc; ++e)
                     if (!((via >> slot_of(e)) & 1u)) (void)mbar_wait(&bars.full[slot_of(e)], use_of(e), ctx);
             }
         } else if (warp < 11) {
             // ------------------------------------------------------------ MMA issuers
-            // S of the next key tile follows PV of this one at once: P lies over S, and MMAs of one
-            // thread run in order.  The whole warp runs the loop and one elected lane issues.
+            // The whole warp runs the loop and one elected lane issues.  S of round k + 2 lies over the P
+            // that PV of round k reads: MMAs of one thread run in order.
             const int x = warp - 9;
             auto wait_w = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, ctx, abort); };
             const uint32_t dO = tmem + kColO + x * 128, dS = tmem + kColS + x * 128;
             const uint64_t dhi = (uint64_t)sdesc_sw128_hi(1024) << 32;
-            const uint64_t q_d = dhi | sdesc_sw128_lo(smem_u32(sm + x * L::kTile), 16);
+            const uint64_t q_d = dhi | sdesc_sw128_lo(smem_u32(sm + x * L::kQTile), 16);
             const uint64_t k_d0 = dhi | sdesc_sw128_lo(smem_u32(sm + L::kOffRing), 16);
             const uint64_t v_d0 = dhi | sdesc_sw128_lo(smem_u32(sm + L::kOffRing), L::kBox);
-            const uint32_t idPV = idesc_bf16_f32(128, D, false, true);
-            uint32_t rc = 0, kq = 0, np = 0;  // entries, Q tiles, P tiles
+            constexpr uint32_t idPV = idesc_bf16_f32(128, D, false, true);
+            uint32_t rc = 0, kq = 0, sr = 0, pr = 0;  // entries, Q tiles, rounds, rounds with P, before the unit
             bool ok = true;
             Unit u;
             for (int it = 0; ok && take_unit(it, u); ++it) {
                 int lkA, lkB;
                 const int nA = key_tiles(u, 0, tq, &lkA), nB = key_tiles(u, 1, tq, &lkB);
                 const int n = max(nA, nB), nx = x ? nB : nA, lk = x ? lkB : lkA;
-                auto issue_s = [&](int b) -> bool {
-                    const uint32_t e = rc + 2 * b;
-                    if (!wait_w(&bars.full[slot_of(e)], use_of(e))) return false;
-                    tc_fence_after();
-                    const uint32_t id = idesc_bf16_f32(128, b == nx - 1 ? lk : kKeys, false, false);
-                    const uint64_t k_d = k_d0 + slot_of(e) * (L::kTile >> 4);
+                auto issue_s = [&](int b) -> bool {  // round b; without an S past the last key tile
+                    const uint32_t j = (sr + b) & 1;
+                    if (b < nx) {
+                        const uint32_t e = rc + 2 * b;
+                        if (!wait_w(&bars.full[slot_of(e)], use_of(e))) return false;
+                        tc_fence_after();
+                        const uint32_t id = idesc_bf16_f32(128, b == nx - 1 ? lk : kK, false, false);
+                        const uint64_t k_d = k_d0 + slot_of(e) * (L::kTile >> 4);
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * L::kBox + (ks & 3) * 32) >> 4;
-                        mma_ss_elect(dS, q_d + off, k_d + off, id, ks > 0 ? 1u : 0u);
+                        for (int ks = 0; ks < D / 16; ++ks)
+                            mma_ss_elect(dS + j * 64, q_d + (((ks >> 2) * L::kQBox + (ks & 3) * 32) >> 4),
+                                         k_d + (((ks >> 2) * L::kBox + (ks & 3) * 32) >> 4), id, ks > 0 ? 1u : 0u);
                     }
-                    mma_commit_elect(&bars.s_full[x]);
+                    mma_commit_elect(&bars.s_full[x][j]);
                     return true;
                 };
                 if (nx > 0) {
-                    ok = wait_w(&bars.q_full[x], kq & 1) && issue_s(0);
+                    ok = wait_w(&bars.q_full[x], kq & 1) && issue_s(0) && issue_s(1);
                     ++kq;
                 }
-                for (int b = 0; ok && b < nx; ++b) {
-                    const uint32_t e = rc + 2 * b + 1;
-                    ok = wait_w(&bars.p_full[x], np & 1) && wait_w(&bars.full[slot_of(e)], use_of(e));
-                    ++np;
+                for (int b = 0; ok && b < nx; ++b, ++pr) {
+                    const uint32_t e = rc + 2 * b + 1, j = (sr + b) & 1;
+                    ok = wait_w(&bars.full[slot_of(e)], use_of(e)) && wait_w(&bars.p_full[x][pr & 1], (pr >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t v_d = v_d0 + slot_of(e) * (L::kTile >> 4);
-                    const int steps = (b == nx - 1 ? lk : kKeys) / 16;
-                    if (steps == kKeys / 16) {
+                    const int steps = (b == nx - 1 ? lk : kK) / 16;
+                    auto pv = [&](int ks) {
+                        mma_ts_elect(dO, dS + j * 64 + ks * 8, v_d + ((ks * 16 * 128) >> 4), idPV,
+                                     (b > 0 || ks > 0) ? 1u : 0u);
+                    };
+                    if (steps == kK / 16) {
 #pragma unroll
-                        for (int ks = 0; ks < kKeys / 16; ++ks)
-                            mma_ts_elect(dO, dS + ks * 8, v_d + ((ks * 16 * 128) >> 4), idPV,
-                                         (b > 0 || ks > 0) ? 1u : 0u);
+                        for (int ks = 0; ks < kK / 16; ++ks) pv(ks);
                     } else {
-                        for (int ks = 0; ks < steps; ++ks)
-                            mma_ts_elect(dO, dS + ks * 8, v_d + ((ks * 16 * 128) >> 4), idPV,
-                                         (b > 0 || ks > 0) ? 1u : 0u);
+                        for (int ks = 0; ks < steps; ++ks) pv(ks);
                     }
-                    if (b + 1 < nx) ok = issue_s(b + 1);
-                    else mma_commit_elect(&bars.o_full[x]);
+                    ok = issue_s(b + 2);
                 }
+                if (nx > 0) sr += nx + 2;
                 // Key tiles that only the other tile has: seen in order and handed back.
                 for (int b = nx; ok && b < n; ++b) {
                     for (int j = 0; ok && j < 2; ++j) {
@@ -294,7 +301,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         } else {
             // ------------------------------------------------------------ V rows not every row sees
             uint32_t rc = 0;
-            uint32_t nl[2][2] = {{0, 0}, {0, 0}};
+            uint32_t nl[2][4] = {};
             Unit u;
             bool dirty[2] = {false, false};
             for (int it = 0; take_unit(it, u); ++it) {
@@ -303,7 +310,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const int n = max(nA, nB);
                 const int last = min(u.first + ut, u.len) - 1;
                 uint16_t* note = notes + (it & 1) * 2 * D;  // [sign][column]; keys from key base on
-                const int base = (u.first / kKeys) * kKeys;
+                const int base = (u.first / kK) * kK;
                 // The unit that used these notes last is done (its softmax warps have left it).
                 if (dirty[it & 1]) {
                     for (int e = lane; e < 2 * D; e += 32) note[e] = kNoKey;
@@ -311,15 +318,15 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     dirty[it & 1] = false;
                     __syncwarp();
                 }
-                const int looked = u.first / kKeys;
+                const int looked = u.first / kK;
                 bool ok = true;
                 for (int b = looked; ok && b < n; ++b) {
                     const uint32_t e = rc + 2 * b + 1;
                     ok = wait_warp(&bars.v_landed[it & 1][b - looked], nl[it & 1][b - looked]++ & 1, ctx, abort);
                     if (!ok) break;
-                    const int k0 = b * kKeys;
+                    const int k0 = b * kK;
                     const int r0 = max(u.first + 1 - k0, 0);
-                    const int r1 = min(((last - k0) / 16 + 1) * 16, kKeys);  // what PV reads
+                    const int r1 = min(((last - k0) / 16 + 1) * 16, kK);  // what PV reads
                     constexpr int kC = D / 8;                                // 16-byte pieces per row
                     bool wrote = false;
                     for (int c0 = 0; c0 < (r1 - r0) * kC; c0 += 32) {
@@ -373,82 +380,82 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const uint32_t colO = tmem + lane_base + kColO + x * 128;
         const uint32_t colS = tmem + lane_base + kColS + x * 128;
         const bool lead = (tid & 127) == 0;  // hands stages and Q back for the tile
-        uint32_t rc = 0, ns = 0, nq = 0;
+        uint32_t rc = 0, sr = 0, pr = 0;  // as the issuer's
         bool ok = true;
         Unit u;
         for (int it = 0; ok && take_unit(it, u); ++it) {
             int lkA, lkB;
             const int nA = key_tiles(u, 0, tq, &lkA), nB = key_tiles(u, 1, tq, &lkB);
-            const int n = max(nA, nB), nx = x ? nB : nA, lk = x ? lkB : lkA;
+            const int n = max(nA, nB), nx = x ? nB : nA;
             const int i = u.first + x * tq + r % tq;  // this row's token
-            const int full_tiles = (u.first + x * tq + 1) / kKeys;  // key tiles that every row sees whole
+            const int full_tiles = (u.first + x * tq + 1) / kK;  // key tiles that every row sees whole
             RowState st;
-            for (int b = 0; b < nx; ++b, ++ns) {
-                ok = wait_warp(&bars.s_full[x], ns & 1, ctx, abort);
+            auto round = [&](int b) { return wait_warp(&bars.s_full[x][(sr + b) & 1], ((sr + b) >> 1) & 1, ctx, abort); };
+            auto give = [&](int e) { mbar_arrive(&bars.empty[slot_of(rc + e)]); };
+            for (int b = 0; b < nx; ++b, ++pr) {
+                ok = round(b);
                 if (!ok) break;
                 tc_fence_after();
-                if (lead) {  // S is done with K, and PV of the tile before with its V
-                    mbar_arrive(&bars.empty[slot_of(rc + 2 * b)]);
-                    if (b > 0) mbar_arrive(&bars.empty[slot_of(rc + 2 * b - 1)]);
+                if (lead) {  // S of this round is done with K, PV of the one before last with its V
+                    give(2 * b);
+                    if (b > 1) give(2 * b - 3);
                     if (b == nx - 1) mbar_arrive(&bars.q_empty[x]);
                 }
-                uint32_t sr[kKeys];
+                const uint32_t col = colS + ((sr + b) & 1) * 64;
+                uint32_t s[kK];  // (columns that S left unwritten are hidden)
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
                 float alpha;
+                tmem_ld32(col, *reinterpret_cast<uint32_t(*)[32]>(s));
+                tmem_ld32(col + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
+                tmem_ld_wait();
                 if (b < full_tiles) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(colS + 32 * c, chunk(sr, c));
-                    tmem_ld_wait();
-                    float mx = max2n(max2n(max32(sr), max32(sr + 32)), max2n(max32(sr + 64), max32(sr + 96)));
-                    alpha = st.raise(mx * sl2);
+                    alpha = st.raise(max2n(max32(s), max32(s + 32)) * sl2);
                     const float nb = st.shift();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 2; ++c) {
                         uint32_t pk[16];
-                        exp32<false, false>(sr + 32 * c, sl2, nb, 0u, nullptr, acc, pk);
-                        tmem_st16(colS + 16 * c, pk);
+                        exp32<false, false>(s + 32 * c, sl2, nb, 0u, nullptr, acc, pk);
+                        tmem_st16(col + 16 * c, pk);
                     }
                 } else {
-                    const int lim = i - b * kKeys;
-                    const int keys = b == nx - 1 ? lk : kKeys;  // columns of S that were computed
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tmem_ld32(colS + 32 * c, chunk(sr, c));  // what S left unwritten is hidden
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (32 * c < keys) mx = max2n(mx, max32_masked(sr + 32 * c, bits_to(lim - 32 * c)));
-                    alpha = st.raise(mx * sl2);
+                    const int lim = i - b * kK;
+                    const uint32_t s0 = bits_to(lim), s1 = bits_to(lim - 32);
+                    alpha = st.raise(max2n(max32_masked(s, s0), max32_masked(s + 32, s1)) * sl2);
                     const float nb = st.shift();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        if (32 * c < keys) {
-                            uint32_t pk[16];
-                            exp32<true, false>(sr + 32 * c, sl2, nb, bits_to(lim - 32 * c), nullptr, acc, pk);
-                            tmem_st16(colS + 16 * c, pk);
-                        }
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pk[16];
+                        exp32<true, false>(s + 32 * c, sl2, nb, c ? s1 : s0, nullptr, acc, pk);
+                        tmem_st16(col + 16 * c, pk);
+                    }
                 }
                 st.l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-                // PV of the tile before is complete (S was committed behind it): O is ours to scale.
-                if (b > 0 && __any_sync(0xffffffffu, alpha != 1.f)) scale_row<D>(colO, alpha);
+                if (b > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    ok = round(b + 1);  // committed behind PV of the round before: O is ours to scale
+                    if (!ok) break;
+                    tc_fence_after();
+                    scale_row<D>(colO, alpha);
+                }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[x]);
+                if (lane == 0) mbar_arrive(&bars.p_full[x][pr & 1]);
             }
             if (!ok) break;
             ok = wait_warp(&bars.v_seen[it & 1], (it >> 1) & 1, ctx, abort);
             if (!ok) break;
             if (nx > 0) {
-                ok = wait_warp(&bars.o_full[x], nq & 1, ctx, abort);
-                ++nq;
+                ok = round(nx) && round(nx + 1);  // all of the unit's PV
                 if (!ok) break;
                 tc_fence_after();
-                if (lead) mbar_arrive(&bars.empty[slot_of(rc + 2 * nx - 1)]);
+                if (lead) {
+                    if (nx > 1) give(2 * nx - 3);
+                    give(2 * nx - 1);
+                }
+                sr += nx + 2;
                 const float inv = 1.f / st.l;
                 const uint16_t* note = notes + (it & 1) * 2 * D;
-                const int key = i - (u.first / kKeys) * kKeys;  // as the notes count
+                const int key = i - (u.first / kK) * kK;  // as the notes count
                 const bool noted = *reinterpret_cast<volatile int*>(&bars.noted[it & 1]) != 0;
                 __nv_bfloat16* dst = out + ((int64_t)(u.hg * tg + r / tq) * total + u.start + i) * D;
 #pragma unroll 1
@@ -511,7 +518,7 @@ cudaError_t packed_tc(const void* q, const void* k, const void* v, const int32_t
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     CUtensorMap tmQ, tmK, tmV;
-    if (!map(&tmQ, q, H, tq, tg) || !map(&tmK, k, Hkv, kKeys, 1) || !map(&tmV, v, Hkv, kKeys, 1))
+    if (!map(&tmQ, q, H, tq, tg) || !map(&tmK, k, Hkv, kK, 1) || !map(&tmV, v, Hkv, kK, 1))
         return cudaErrorInvalidValue;
     if (cudaError_t e = ensure_smem<packed_tc_kernel<D>>(L::kBytes); e != cudaSuccess) return e;
     // every sequence has at most one unit that is not full
