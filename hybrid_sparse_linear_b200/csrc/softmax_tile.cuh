@@ -4,15 +4,14 @@
 //
 // The maximum is kept stale until a row's new one exceeds it by more than 8 in log2 units: a
 // probability then stays below 2^8, which cancels in O / l, and the accumulator is rescaled only
-// in the rare step that passes the threshold.  Three of four pairs of exponentials go to the
-// multi-function unit and one to the FMA pipe (fastexp.cuh): a tile's 16384 exponentials take
-// 1024 cycles of the former alone, as long as its matrix products.
+// in the rare step that passes the threshold.  All exponentials go to the multi-function unit: it is
+// busy 58 % of the time, and the issue slots are what runs short, of which a pair of FMA-pipe
+// exponentials (fastexp.cuh) takes about ten (one pair in four there: 4 % slower at 32768 tokens).
 //
-// A NaN or +infinity among a row's visible logits makes its sum NaN (the maximum passes NaN on),
-// whatever the exponentials make of it; a hidden position is left out by selection.
+// A NaN or +infinity among a row's visible logits makes its sum NaN (the maximum passes NaN on); a
+// hidden position is left out by selection.
 #pragma once
 
-#include "fastexp.cuh"
 #include "ptx.cuh"
 
 namespace sala {
@@ -21,7 +20,6 @@ namespace smx {
 using namespace ptx;
 
 constexpr int kKeys = 128;      // columns of a tile
-constexpr int kPolyEvery = 4;   // one pair in kPolyEvery takes the FMA-pipe exponential
 constexpr float kGrow = 8.f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -41,12 +39,25 @@ __device__ __forceinline__ float max3n(float a, float b, float c) {
     return d;
 }
 
+// mbar_try_wait that may sleep for up to 20 us before it answers, so that waiting warps leave the issue
+// slots to the working ones.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    return ok != 0;
+}
 // A wait that ends early once the block winds down; a timeout starts the wind-down.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, const DevCtx& ctx,
                                               volatile int* abort) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!mbar_try_wait_long(bar, parity)) {
         if (*abort) return false;
         if (globaltimer_ns() - t0 > ctx.wait_limit_ns) {
             flag(ctx, kStatusTimeout);
@@ -102,14 +113,8 @@ __device__ __forceinline__ void exp32(const uint32_t* s, float sl2, float nb, ui
         const int k = 2 * q;
         float y0, y1, p0, p1;
         fma2_bcast(y0, y1, __uint_as_float(s[k]), __uint_as_float(s[k + 1]), sl2, nb);
-        if (!kMasked && q % kPolyEvery == kPolyEvery - 1) {
-            p0 = y0;
-            p1 = y1;
-            exp2_poly2(p0, p1);
-        } else {
-            p0 = ex2(y0);
-            p1 = ex2(y1);
-        }
+        p0 = ex2(y0);
+        p1 = ex2(y1);
         if (kMasked) {
             p0 = ((seen >> k) & 1u) ? p0 : 0.f;
             p1 = ((seen >> (k + 1)) & 1u) ? p1 : 0.f;
