@@ -150,4 +150,74 @@ __device__ __forceinline__ PackedTile find_packed_tile(const int32_t* cu, int B,
     return t;
 }
 
+// The tiles of `rows` rows (a power of two up to 256) over all sequences, those that begin latest in
+// their sequence -- whose causal rows are longest -- first: in levels of 256 rows from the longest
+// sequence's last down, and inside a level sequence by sequence.  One converged warp walks them in
+// ascending order.
+struct PackedOrder {
+    static constexpr int kLevel = 256;
+    const int32_t* cu;
+    int B, total, rows, lane;
+    int level;        // the level that holds tiles [before, before + n)
+    int64_t before, n;
+
+    // Tiles of sequence b in a level.
+    __device__ __forceinline__ int tiles_in(int len, int lv) const {
+        const int left = min(len - lv * kLevel, kLevel);
+        return left > 0 ? (left + rows - 1) / rows : 0;
+    }
+    __device__ __forceinline__ int len_of(int b, int* start) const {
+        bool bad = false;
+        return b < B ? packed_len(cu, b, total, start, &bad) : 0;
+    }
+    __device__ __forceinline__ int64_t count(int lv) const {
+        int64_t s = 0;
+        int start;
+        for (int b = lane; b < B; b += 32) s += tiles_in(len_of(b, &start), lv);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        return s;
+    }
+    // report: flag offsets that are out of order.
+    __device__ __forceinline__ PackedOrder(const int32_t* cu, int B, int total, int rows, int lane,
+                                           const DevCtx& ctx, bool report)
+        : cu(cu), B(B), total(total), rows(rows), lane(lane), before(0) {
+        int longest = 0, start;
+        bool bad = false;
+        for (int b = lane; b < B; b += 32) longest = max(longest, packed_len(cu, b, total, &start, &bad));
+        if (report && bad) flag(ctx, kStatusBounds);
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        level = longest > 0 ? (longest - 1) / kLevel : -1;
+        n = level >= 0 ? count(level) : 0;
+    }
+    // Tile i (not below the i of the last call); len = 0 when there are no more.
+    __device__ __forceinline__ PackedTile at(int64_t i) {
+        while (level >= 0 && i >= before + n) {
+            before += n;
+            n = --level >= 0 ? count(level) : 0;
+        }
+        if (level < 0) return {0, 0, 0};
+        int64_t from = before;
+        for (int b0 = 0; b0 < B; b0 += 32) {
+            int start = 0;
+            const int len = len_of(b0 + lane, &start), k = tiles_in(len, level);
+            int inc = k;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += up;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, from + inc > i);
+            if (hit) {
+                const int w = __ffs((int)hit) - 1;
+                const int end = __shfl_sync(0xffffffffu, inc, w);
+                return {__shfl_sync(0xffffffffu, start, w), __shfl_sync(0xffffffffu, len, w),
+                        level * kLevel + (int)(from + end - 1 - i) * rows};
+            }
+            from += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        return {0, 0, 0};
+    }
+};
+
 }  // namespace sala

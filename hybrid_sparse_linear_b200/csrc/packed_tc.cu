@@ -22,8 +22,8 @@
 // epilogue gives them back to the rows behind that key.
 //
 // Roles (384 threads, persistent, one CTA per SM): warps 0-3 softmax and epilogue of tile A, 4-7 of
-// tile B (thread = row); warp 8 finds the units and issues the TMA loads; warps 9 and 10 issue the
-// MMAs of tiles A and B; warp 11 looks through V.  Completions: the issuer commits once per round,
+// tile B (thread = row); warp 8 issues the TMA loads; warps 9 and 10 issue the MMAs of tiles A and B;
+// warp 11 finds the units, two ahead, and looks through V.  Completions: the issuer commits once per round,
 // after PV(k) and S(k + 2), so the commit of round k + 2 says that both are done; two more rounds
 // without an S close a unit.  The softmax hands K and V stages back as it sees the commits.  Every
 // wait is bounded; a timeout sets the status word and all roles wind down.
@@ -41,7 +41,7 @@ using namespace smx;
 
 constexpr int kThreads = 384;
 constexpr int kK = 64;   // keys per tile
-constexpr int kConsumerWarps = 11;  // all but the unit finder
+constexpr int kWarps = kThreads / 32;
 
 template <int D>
 struct Layout {
@@ -49,9 +49,10 @@ struct Layout {
     static constexpr int kQTile = (D / 64) * kQBox;
     static constexpr int kBox = kK * 128;             // [kK rows x 64 columns]
     static constexpr int kTile = (D / 64) * kBox;     // a K or V tile
-    static constexpr int kSlots = 10;                 // ring of K and V tiles
+    static constexpr int kSlots = 9;                  // ring of K and V tiles
     static constexpr int kOffRing = 2 * kQTile;
-    static constexpr int kOffNotes = kOffRing + kSlots * kTile;
+    static constexpr int kOffStage = kOffRing + kSlots * kTile;  // per softmax warp: 32 rows x 32 columns
+    static constexpr int kOffNotes = kOffStage + 8 * 2048;
     static constexpr int kNoteBytes = 2 * 2 * D * 2;  // unit parity x sign x column, uint16
     static constexpr int kBytes = kOffNotes + kNoteBytes + 1024;  // + alignment of the base
 };
@@ -124,7 +125,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 mbar_init(&bars.p_full[x][j], 4);
             }
             mbar_init(&bars.unit_full[x], 1);
-            mbar_init(&bars.unit_empty[x], kConsumerWarps);
+            mbar_init(&bars.unit_empty[x], kWarps);
             mbar_init(&bars.fin[x], 1);
             bars.noted[x] = 0;
         }
@@ -159,23 +160,12 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     if (warp >= 8) {
         set_regs_down<72>();
         if (warp == 8) {
-            // ------------------------------------------------------------ units and loads
+            // ------------------------------------------------------------ loads
             uint32_t rc = 0, kq[2] = {0, 0};
             uint32_t nl[2][4] = {};  // uses of v_landed
-            uint32_t via = 0;                      // slots whose last load went to v_landed
-            for (int it = 0;; ++it) {
-                // Every other round runs the CTAs backwards: units come longest first within a
-                // sequence, and the turn evens out what the CTAs get.
-                const int c = (it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-                const int64_t i = (int64_t)it * gridDim.x + c;
-                const PackedTile t = find_packed_tile(cu, B, total, i / n_hg, ut, lane, ctx, i == 0);
-                Unit u{t.start, t.len, t.first, (int)(i % n_hg)};
-                if (it >= 2 && !wait_warp(&bars.unit_empty[it & 1], ((it - 2) >> 1) & 1, ctx, abort)) break;
-                if (lane == 0) {
-                    bars.unit[it & 1] = u;
-                    mbar_arrive(&bars.unit_full[it & 1]);
-                }
-                if (u.len == 0) break;
+            uint32_t via = 0;        // slots whose last load went to v_landed
+            Unit u;
+            for (int it = 0; take_unit(it, u); ++it) {
                 int lk;
                 const int nA = key_tiles(u, 0, tq, &lk), nB = key_tiles(u, 1, tq, &lk);
                 const int n = max(nA, nB);
@@ -213,7 +203,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         if (e == 0) load_q(1);
                     }
                 }
-                rc = __shfl_sync(0xffffffffu, rc, 0);
+                leave_unit(it);
                 if (__shfl_sync(0xffffffffu, stop, 0)) break;
             }
             if (lane == 0) {  // drain: every copy this warp started has landed before the block exits
@@ -299,7 +289,22 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             (void)mbar_wait(&bars.fin[x], 0, ctx);
             __syncwarp();
         } else {
-            // ------------------------------------------------------------ V rows not every row sees
+            // ------------------------------------------------------------ units; V rows not every row sees
+            PackedOrder order(cu, B, total, ut, lane, ctx, blockIdx.x == 0);
+            auto publish = [&](int it) {
+                // Every other round runs the CTAs backwards: units come longest first, and the turn evens
+                // out what the CTAs get.
+                const int c = (it & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+                const int64_t i = (int64_t)it * gridDim.x + c;
+                const PackedTile t = order.at(i / n_hg);
+                if (it >= 2 && !wait_warp(&bars.unit_empty[it & 1], ((it - 2) >> 1) & 1, ctx, abort)) return;
+                if (lane == 0) {
+                    bars.unit[it & 1] = Unit{t.start, t.len, t.first, (int)(i % n_hg)};
+                    mbar_arrive(&bars.unit_full[it & 1]);
+                }
+            };
+            publish(0);
+            publish(1);
             uint32_t rc = 0;
             uint32_t nl[2][4] = {};
             Unit u;
@@ -369,6 +374,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 rc += 2 * n;
                 leave_unit(it);
                 if (!ok) break;
+                publish(it + 2);
             }
         }
     } else {
@@ -457,7 +463,9 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint16_t* note = notes + (it & 1) * 2 * D;
                 const int key = i - (u.first / kK) * kK;  // as the notes count
                 const bool noted = *reinterpret_cast<volatile int*>(&bars.noted[it & 1]) != 0;
-                __nv_bfloat16* dst = out + ((int64_t)(u.hg * tg + r / tq) * total + u.start + i) * D;
+                // 32 columns at a time through shared memory: a row's 64 bytes are then stored by four
+                // neighbouring lanes, whole sectors, instead of 16 bytes of 32 rows at once.
+                uint8_t* stage = sm + L::kOffStage + warp * 2048;
 #pragma unroll 1
                 for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
@@ -473,17 +481,28 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                             o[q] = __float_as_uint(y);
                         }
                     }
-                    if (i < u.len) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t w[4];
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                w[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
-                                                   __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
-                            *reinterpret_cast<uint4*>(dst + c0 + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
+                                               __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
+                        *reinterpret_cast<uint4*>(stage + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int sr_row = 8 * q + (lane >> 2);           // of the warp's 32 rows
+                        const int rr = (warp & 3) * 32 + sr_row, token = u.first + x * tq + rr % tq;
+                        const uint4 v = *reinterpret_cast<const uint4*>(
+                            stage + sr_row * 64 + (((lane & 3) ^ ((sr_row >> 1) & 3)) << 4));
+                        if (token < u.len)
+                            *reinterpret_cast<uint4*>(out + ((int64_t)(u.hg * tg + rr / tq) * total + u.start + token) * D +
+                                                      c0 + 8 * (lane & 3)) = v;
+                    }
+                    __syncwarp();
                 }
                 tc_fence_before();
             }
