@@ -2,18 +2,16 @@
 // bf16 queries; the cache in bf16 or as 8-bit codes with one scale per row.
 //
 // The G * T query rows of a KV head are its M: rows (head g, token t) are contiguous in q.  Above 128
-// rows (wide) an item takes 256, two tiles A and B that share every K and V tile of 128 keys.  Up to
-// 128 rows (narrow) there is one tile of rows, and A takes the even, B the odd 64-key tiles of the
-// CTA's run, each with its own ring and accumulator, joined at the end.  Either way two chains
-// S -> softmax -> PV run against each other; the narrow form also has two S buffers per chain, so the
-// next S does not wait for this one's PV (its chain is short and latency counts; the wide form fills
-// its TMEM with 128-column S tiles, which feed the tensor core better).
+// rows (wide) an item takes 256, two tiles A and B that share every K and V tile.  Up to 128 rows
+// (narrow) there is one tile of rows, and A takes the even, B the odd key tiles of the CTA's run, each
+// with its own ring and accumulator, joined at the end.  Either way two chains of 64-key steps run
+// beside each other, each with two S buffers, so that the next S does not wait for this one's PV.
 // Work is divided by key tiles (tree_plan.cuh), so a single sequence uses every SM.
 //
 // Bound: HBM for few rows (a key and value row are read once per 256 query rows: 4 G T d flops
 // against 4 d bytes, 2 (d + 4) in 8 bits), the tensor pipe from about T = 16 at G = 16.
 //
-// 8-bit caches.  Codes are at most 8 bits wide, so each is a bf16 number exactly; a warpgroup turns
+// 8-bit caches.  Codes are at most 8 bits wide, so each is a bf16 number exactly; eight warps turn
 // the raw bytes of a tile into bf16 tiles in shared memory and the matrix products run as for bf16.
 // The scales never touch the tiles: a key's scale multiplies its column of S, a value's scale its
 // column of P (before P's one rounding to bf16, after the row sum), both in 32 bits.
@@ -26,7 +24,7 @@
 //
 // Roles: warps 0-3 softmax and epilogue of tile A, 4-7 of B; 8 walks the items and loads (TMA for
 // bf16 tiles, bulk copies for codes and scales); 9 and 10 issue the MMAs of A and B; 11 looks through
-// V (bf16); 12-15 (8-bit caches only) convert.  Every wait is bounded.
+// V (bf16); 12-19 (8-bit caches only) convert.  Every wait is bounded.
 #include <type_traits>
 
 #include "kv_format.cuh"
@@ -40,27 +38,25 @@ namespace {
 using namespace ptx;
 using namespace smx;
 
-constexpr int kConvThreads = 128;
-constexpr int kPad = 3;  // beginning an item (Q, the first tiles' chain, the epilogue) costs about three tiles
+constexpr int kK = 64;              // keys per tile: a page
+constexpr int kConvThreads = 256;
+constexpr int kPad = 4;  // beginning an item (Q, the first tiles' chain, the epilogue) costs about four tiles
 
 template <int D, KvFormat F, bool kWide>
 struct Layout {
     static constexpr bool kCodes = F != KvFormat::Same;
-    static constexpr int kThreads = kCodes ? 512 : 384;
-    static constexpr int kRegsSoft = kCodes ? 200 : 216, kRegsRest = kCodes ? 56 : 72;
+    static constexpr int kThreads = kCodes ? 640 : 384;
+    static constexpr int kRegsSoft = kCodes ? 144 : 216, kRegsRest = kCodes ? 64 : 72;
     static constexpr int kRows = kWide ? 256 : 128;          // query rows per item
-    static constexpr int kK = kWide ? 128 : 64;              // keys per tile
-    static constexpr int kPages = kK / kPage;
-    static constexpr int kBufs = kWide ? 1 : 2;              // S buffers per tile of rows
     static constexpr int kQBox = 128 * 128;                  // [128 rows x 64 columns] bf16, swizzled
     static constexpr int kQTile = (D / 64) * kQBox;
     static constexpr int kBox = kK * 128;                    // [kK rows x 64 columns]
     static constexpr int kTile = (D / 64) * kBox;            // a K or V tile
     static constexpr int kRaw = kK * D;                      // the codes of one
     // K and V tiles: one ring that both tiles of rows use, or one for each.
-    static constexpr int kRing = (kWide ? (kCodes ? 3 : 5) : (kCodes ? 4 : 5)) * (128 / D);
+    static constexpr int kRing = (kWide ? (kCodes ? 6 : 9) : (kCodes ? 4 : 5)) * (128 / D);
     static constexpr int kSlots = kWide ? kRing : 2 * kRing;
-    static constexpr int kRawSlots = kCodes ? (kWide ? 3 : 6) * (128 / D) : 0;
+    static constexpr int kRawSlots = kCodes ? 6 * (128 / D) : 0;
     // The tiles first (each 1024-byte aligned), then the small parts.
     static constexpr int kOffRing = (kWide ? 2 : 1) * kQTile;
     static constexpr int kOffRaw = kOffRing + kSlots * kTile;
@@ -82,7 +78,7 @@ struct Item {
 struct Look {
     int slot;     // where it is
     int k0, ctx;  // its first key; the sequence's context length
-    int pages;    // bit 0, 1: the half's page holds keys
+    int have;     // whether the table holds its page
     int it, last;  // the item, and whether this is its last tile with drafts
 };
 
@@ -99,8 +95,8 @@ struct Bars {
     uint64_t fin[2];
     Item item[2];
     Look look[2];
-    int pages[2][8];                     // as Look::pages, per ring and key tile (a ring holds at most 6)
-    int raw_pages[L::kRawSlots + 1];
+    int have[2][16];                     // as Look::have, per ring and key tile (a ring holds at most 10)
+    int raw_have[L::kRawSlots + 1];
     int noted_it;                        // the item that the notes belong to
     uint32_t tmem_base;
     int abort;
@@ -116,7 +112,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     constexpr bool kCodes = L::kCodes;
     constexpr uint32_t kRing = L::kRing, kSlots = L::kSlots, kRawSlots = kCodes ? L::kRawSlots : 1;
     constexpr uint32_t kColO = 0, kColS = 256;
-    constexpr int kK = L::kK, kBufs = L::kBufs;
     extern __shared__ __align__(1024) uint8_t sm[];  // all of the block's shared memory
     Bars<L>& bars = *reinterpret_cast<Bars<L>*>(sm + L::kOffBars);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -151,7 +146,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             mbar_init(&bars.look_free[x], 1);
             mbar_init(&bars.v_seen[x], 1);
             mbar_init(&bars.item_full[x], 1);
-            mbar_init(&bars.item_empty[x], 10 + (kCodes ? 4 : 0));  // softmax, issuers, converters
+            mbar_init(&bars.item_empty[x], 10 + (kCodes ? 8 : 0));  // softmax, issuers, converters
             mbar_init(&bars.fin[x], 1);
         }
         mbar_init(&bars.q_empty, 2);
@@ -220,62 +215,48 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     }
                 }
                 ++kq;
-                const int keys = c.ctx + s.T;
                 int ids = -1;
                 for (int i = 0; ok && i < n; ++i) {
                     const int t = t0 + i;
-                    constexpr int kP = L::kPages, kBatch = 32 / kP;  // key tiles that 32 pages make
-                    if (i % kBatch == 0) ids = page_of(pages, c.b, kP * t + lane);
-                    int id[2] = {0, 0};
-                    int have = 0;
-#pragma unroll
-                    for (int h = 0; h < kP; ++h) {
-                        id[h] = __shfl_sync(0xffffffffu, ids, kP * (i % kBatch) + h);
-                        if (t * kK + h * kPage < keys) {
-                            if (id[h] >= 0) have |= 1 << h;
-                            else if (lane == 0) flag(ctx, kStatusBounds);  // left out
-                        }
-                    }
+                    if ((i & 31) == 0) ids = page_of(pages, c.b, t + lane);
+                    const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+                    const bool have = id >= 0;
+                    if (!have && lane == 0) flag(ctx, kStatusBounds);  // left out
+                    const int row = (id * s.Hkv + c.g) * kPage;
                     const bool drafts = (t + 1) * kK > c.ctx;  // keys that some row does not see
                     for (int j = 0; ok && j < 2; ++j) {  // K, V
-                        const int row[2] = {(id[0] * s.Hkv + c.g) * kPage, (id[1] * s.Hkv + c.g) * kPage};
                         if constexpr (kCodes) {
                             const uint32_t q = raw_of(rr);
                             if (rr >= kRawSlots && !(ok = wait_warp(&bars.raw_empty[q], raw_use(rr - kRawSlots), ctx, abort)))
                                 break;
                             ++rr;
                             if (lane == 0) {
-                                bars.raw_pages[q] = have;
-                                mbar_arrive_expect_tx(&bars.raw_full[q], __popc(have) * (kPage * D + kPage * 4));
-                                const uint8_t* codes = static_cast<const uint8_t*>(j ? pages.v : pages.k);
-                                const float* scales = j ? pages.v_scale : pages.k_scale;
-                                for (int h = 0; h < kP; ++h)
-                                    if ((have >> h) & 1) {
-                                        bulk_load_g2s(sm + L::kOffRaw + q * L::kRaw + h * kPage * D,
-                                                      codes + (int64_t)row[h] * D, kPage * D, &bars.raw_full[q]);
-                                        bulk_load_g2s(sm + L::kOffRawScale + (q * kK + h * kPage) * 4,
-                                                      scales + row[h], kPage * 4, &bars.raw_full[q]);
-                                    }
+                                bars.raw_have[q] = have;
+                                mbar_arrive_expect_tx(&bars.raw_full[q], have ? L::kRaw + kK * 4 : 0);
+                                if (have) {
+                                    bulk_load_g2s(sm + L::kOffRaw + q * L::kRaw,
+                                                  static_cast<const uint8_t*>(j ? pages.v : pages.k) + (int64_t)row * D,
+                                                  L::kRaw, &bars.raw_full[q]);
+                                    bulk_load_g2s(sm + L::kOffRawScale + q * kK * 4,
+                                                  (j ? pages.v_scale : pages.k_scale) + row, kK * 4, &bars.raw_full[q]);
+                                }
                             }
                         } else {
                             const bool odd = !kWide && (i & 1);
                             const uint32_t e = odd ? rc[1] : rc[0], q = slot_of(odd, e);
                             if (e >= kRing && !(ok = wait_warp(&bars.empty[q], use_of(e - kRing), ctx, abort)))
                                 break;
-                            const bool look = j == 1 && (drafts || have != (1 << kP) - 1);
+                            const bool look = j == 1 && (drafts || !have);
                             if (look && looks >= 2 &&
                                 !(ok = wait_warp(&bars.look_free[looks & 1], ((looks - 2) >> 1) & 1, ctx, abort)))
                                 break;
                             if (lane == 0) {
                                 uint64_t* fb = look ? &bars.v_landed[looks & 1] : &bars.full[q];
-                                if (j == 0) bars.pages[odd][(e >> 1) & 7] = have;
+                                if (j == 0) bars.have[odd][(e >> 1) & 15] = have;
                                 if (look) bars.look[looks & 1] = Look{(int)q, t * kK, c.ctx, have, it, drafts && i == n - 1};
-                                mbar_arrive_expect_tx(fb, __popc(have) * (L::kTile / kP));
-                                for (int h = 0; h < kP; ++h)
-                                    if ((have >> h) & 1)
-                                        for (int p = 0; p < D / 64; ++p)
-                                            tma_load_2d(slot_ptr(q) + p * L::kBox + h * (L::kBox / kP),
-                                                        j ? &tmV : &tmK, fb, 64 * p, row[h]);
+                                mbar_arrive_expect_tx(fb, have ? L::kTile : 0);
+                                for (int p = 0; have && p < D / 64; ++p)
+                                    tma_load_2d(slot_ptr(q) + p * L::kBox, j ? &tmV : &tmK, fb, 64 * p, row);
                             }
                             via = (via & ~(1u << q)) | ((look ? 1u : 0u) << q);
                             looks += look ? 1 : 0;
@@ -311,7 +292,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
         } else if (warp < 11) {
             // ------------------------------------------------------------ MMA issuers
-            // Order per tile: PV of a key tile, then S of the one kBufs further, which lies over the P
+            // Order per tile: PV of a key tile, then S of the one two further, which lies over the P
             // that this PV read; MMAs of one thread run in order.  The whole warp runs the loop and one
             // elected lane issues.
             const int x = warp - 9;
@@ -329,7 +310,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             for (int it = 0; ok && take_item(it, m); ++it) {
                 const int nx = my_tiles(m.n, x);
                 auto issue_s = [&](int k) -> bool {
-                    const uint32_t e = rc + 2 * k, q = slot_of(x, e), j = (a + k) % kBufs;
+                    const uint32_t e = rc + 2 * k, q = slot_of(x, e), j = (a + k) & 1;
                     if (!wait_w(&bars.full[q], use_of(e))) return false;
                     tc_fence_after();
                     const uint64_t k_d = k_d0 + q * (L::kTile >> 4);
@@ -342,10 +323,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     return true;
                 };
                 ok = wait_w(&bars.q_full[kWide ? x : 0], it & 1);
-                for (int k = 0; ok && k < kBufs && k < nx; ++k) ok = issue_s(k);
+                for (int k = 0; ok && k < 2 && k < nx; ++k) ok = issue_s(k);
                 for (int k = 0; ok && k < nx; ++k) {
-                    const uint32_t e = rc + 2 * k + 1, q = slot_of(x, e), j = (a + k) % kBufs;
-                    ok = wait_w(&bars.p_full[x][j], ((a + k) / kBufs) & 1) && wait_w(&bars.full[q], use_of(e));
+                    const uint32_t e = rc + 2 * k + 1, q = slot_of(x, e), j = (a + k) & 1;
+                    ok = wait_w(&bars.p_full[x][j], ((a + k) / 2) & 1) && wait_w(&bars.full[q], use_of(e));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t v_d = v_d0 + q * (L::kTile >> 4);
@@ -355,7 +336,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                                      (k > 0 || ks > 0) ? 1u : 0u);
                     mma_commit_elect(&bars.pv_done[x][j]);
                     mma_commit_elect(&bars.empty[q]);
-                    if (k + kBufs < nx) ok = issue_s(k + kBufs);
+                    if (k + 2 < nx) ok = issue_s(k + 2);
                 }
                 rc += 2 * nx;
                 a += nx;
@@ -379,7 +360,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         const int r = (c0 + lane) / kC, c = (c0 + lane) % kC, j = v.k0 + r - v.ctx;
                         uint4* p = reinterpret_cast<uint4*>(tile + (c >> 3) * L::kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
                         bool bad = false;
-                        if (v.k0 + r >= keys || !((v.pages >> (r >> 6)) & 1)) *p = make_uint4(0u, 0u, 0u, 0u);
+                        if (v.k0 + r >= keys || !v.have) *p = make_uint4(0u, 0u, 0u, 0u);
                         else if (j >= 0) bad = any_nonfinite8(*p);
                         unsigned todo = __ballot_sync(0xffffffffu, bad);
                         if (todo == 0u) continue;
@@ -460,7 +441,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         if (ct < kK)
                             reinterpret_cast<float*>(sm + L::kOffScale)[q * kK + ct] =
                                 reinterpret_cast<const float*>(sm + L::kOffRawScale)[raw_of(rr) * kK + ct];
-                        if (ct == 0 && !(i & 1)) bars.pages[odd][(e2 >> 1) & 7] = bars.raw_pages[raw_of(rr)];
+                        if (ct == 0 && !(i & 1)) bars.have[odd][(e2 >> 1) & 15] = bars.raw_have[raw_of(rr)];
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
@@ -496,9 +477,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             RowState st;
             for (int k = 0; k < nx; ++k) {
                 const int i = nth_tile(k, x), k0 = (m.tile + i) * kK;
-                const uint32_t e = rc + 2 * k, qk = slot_of(x, e), qv = slot_of(x, e + 1), j = (a + k) % kBufs;
+                const uint32_t e = rc + 2 * k, qk = slot_of(x, e), qv = slot_of(x, e + 1), j = (a + k) & 1;
                 const uint32_t col = colS + j * 64;
-                ok = wait_warp(&bars.s_full[x][j], ((a + k) / kBufs) & 1, ctx, abort);
+                ok = wait_warp(&bars.s_full[x][j], ((a + k) / 2) & 1, ctx, abort);
                 if (kCodes && ok) ok = wait_warp(&bars.full[qk], use_of(e), ctx, abort);  // (done: for its scales)
                 if (!ok) break;
                 tc_fence_after();
@@ -508,7 +489,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < kK / 32; ++c) tmem_ld32(col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
-                    const int have = bars.pages[ring_of(x)][(e >> 1) & 7];
+                    const bool have = bars.have[ring_of(x)][(e >> 1) & 15] != 0;
                     tmem_ld_wait();
                     if constexpr (kCodes) {
                         const float* ks = reinterpret_cast<const float*>(sm + L::kOffScale) + qk * kK;
@@ -524,7 +505,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         give(qk);
                     }
                     const float* vs = reinterpret_cast<const float*>(sm + L::kOffScale) + qv * kK;
-                    if (k0 + kK <= m.ctx && have == (1 << L::kPages) - 1) {
+                    if (k0 + kK <= m.ctx && have) {
                         float mx = max32(sr);
 #pragma unroll
                         for (int c = 1; c < kK / 32; ++c) mx = max2n(mx, max32(sr + 32 * c));
@@ -545,7 +526,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                             const int d0 = k0 + 32 * c - m.ctx;  // draft number of the chunk's first key
                             const uint32_t drafts = d0 >= 64 ? 0u : d0 >= 0 ? (uint32_t)(bits >> d0)
                                                   : d0 > -32 ? (uint32_t)(bits << -d0) : 0u;
-                            seen[c] = ((have >> (c >> 1)) & 1) ? (bits_to(-d0 - 1) | drafts) : 0u;
+                            seen[c] = have ? (bits_to(-d0 - 1) | drafts) : 0u;
                             mx = max2n(mx, max32_masked(sr + 32 * c, seen[c]));
                         }
                         alpha = st.raise(mx * sl2);
@@ -571,7 +552,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 if (!kWide && x == 1 && k == 0 && n_two > 0) ok = wait_warp(&bars.merged, (n_two - 1) & 1, ctx, abort);
                 if (ok && k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                     const uint32_t b = a + k - 1;  // the PV before has to be done with O
-                    ok = wait_warp(&bars.pv_done[x][b % kBufs], (b / kBufs) & 1, ctx, abort);
+                    ok = wait_warp(&bars.pv_done[x][b & 1], (b / 2) & 1, ctx, abort);
                     if (ok) {
                         tc_fence_after();
                         scale_row<D>(colO, alpha);
@@ -596,7 +577,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             rc += 2 * nx;
             a += nx;
             if (nx > 0) {
-                ok = wait_warp(&bars.pv_done[x][(a - 1) % kBufs], ((a - 1) / kBufs) & 1, ctx, abort);
+                ok = wait_warp(&bars.pv_done[x][(a - 1) & 1], ((a - 1) / 2) & 1, ctx, abort);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -705,9 +686,9 @@ cudaError_t tree_tc(const void* q, const KvPages& pages, const uint64_t* masks, 
     constexpr int bytes = L::kOffBars + (int)sizeof(Bars<L>);
     if (cudaError_t e = ensure_smem<tree_tc_kernel<D, F, kWide>>(bytes); e != cudaSuccess) return e;
     s.n_rt = kWide ? tree::row_tiles(s.rows, L::kRows) : 1;
-    s.kt = L::kK;
+    s.kt = kK;
     s.pad = kPad;
-    const int tiles = (s.max_ctx + s.T + L::kK - 1) / L::kK;
+    const int tiles = (s.max_ctx + s.T + kK - 1) / kK;
     const long long most = (long long)s.B * s.Hkv * s.n_rt * tiles;
     const int sms = device_sm_count();
     const int n_cta = most < sms ? (int)most : sms;
