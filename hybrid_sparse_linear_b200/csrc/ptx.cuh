@@ -345,5 +345,16 @@ __device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
         : "f"(b0), "f"(b1));
 }
 
+// (a0, a1) *= (b0, b1) on the packed two-wide fp32 path.
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 xa, xb;\n\t"
+        "mov.b64 xa, {%0, %1};\n\t"
+        "mov.b64 xb, {%2, %3};\n\t"
+        "mul.rn.f32x2 xa, xa, xb;\n\t"
+        "mov.b64 {%0, %1}, xa;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
+}
+
 }  // namespace ptx
 }  // namespace sala

@@ -108,6 +108,7 @@ __device__ __forceinline__ uint32_t bits_to(int lim) {
 template <bool kMasked, bool kScaled>
 __device__ __forceinline__ void exp32(const uint32_t* s, float sl2, float nb, uint32_t seen, const float* vs,
                                       float (&acc)[4], uint32_t (&pk)[16]) {
+    [[maybe_unused]] float4 v4;
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
         const int k = 2 * q;
@@ -122,9 +123,8 @@ __device__ __forceinline__ void exp32(const uint32_t* s, float sl2, float nb, ui
         if (q & 1) add2(acc[2], acc[3], p0, p1);
         else add2(acc[0], acc[1], p0, p1);
         if (kScaled) {
-            const float2 v = *reinterpret_cast<const float2*>(vs + k);
-            p0 *= v.x;
-            p1 *= v.y;
+            if ((q & 1) == 0) v4 = *reinterpret_cast<const float4*>(vs + k);
+            mul2(p0, p1, (q & 1) ? v4.z : v4.x, (q & 1) ? v4.w : v4.y);
             if (kMasked) {  // a hidden row's scale may be anything
                 p0 = ((seen >> k) & 1u) ? p0 : 0.f;
                 p1 = ((seen >> (k + 1)) & 1u) ? p1 : 0.f;

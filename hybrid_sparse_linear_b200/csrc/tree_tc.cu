@@ -54,9 +54,9 @@ struct Layout {
     static constexpr int kTile = (D / 64) * kBox;            // a K or V tile
     static constexpr int kRaw = kK * D;                      // the codes of one
     // K and V tiles: one ring that both tiles of rows use, or one for each.
-    static constexpr int kRing = (kWide ? (kCodes ? 6 : 9) : (kCodes ? 4 : 5)) * (128 / D);
+    static constexpr int kRing = (kWide ? (kCodes ? 6 : 8) : (kCodes ? 4 : 5)) * (128 / D);
     static constexpr int kSlots = kWide ? kRing : 2 * kRing;
-    static constexpr int kRawSlots = kCodes ? 6 * (128 / D) : 0;
+    static constexpr int kRawSlots = kCodes ? 5 * (128 / D) : 0;
     // The tiles first (each 1024-byte aligned), then the small parts.
     static constexpr int kOffRing = (kWide ? 2 : 1) * kQTile;
     static constexpr int kOffRaw = kOffRing + kSlots * kTile;
@@ -64,8 +64,9 @@ struct Layout {
     static constexpr int kOffScale = kOffRawScale + kRawSlots * kK * 4;
     static constexpr int kOffNotes = kOffScale + (kCodes ? kSlots * kK * 4 : 0);
     static constexpr int kNoteBytes = kCodes ? 0 : 2 * D * 8;    // sign x column, a bit per draft
-    static constexpr int kOffMerge = kOffNotes + kNoteBytes;     // (maximum, sum) of tile B's rows
-    static constexpr int kOffBars = kOffMerge + (kWide ? 0 : 128 * 8);
+    static constexpr int kOffMerge = kOffNotes + kNoteBytes;     // narrow: both tiles' (maximum, sum) per row
+    static constexpr int kOffStage = kOffMerge + (kWide ? 0 : 2 * 128 * 8);  // per softmax warp: 32 rows of 64 bytes
+    static constexpr int kOffBars = kOffStage + 8 * 2048;
 };
 
 // An item's part in this CTA's run.
@@ -90,7 +91,7 @@ struct Bars {
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // per tile and S buffer
     uint64_t v_landed[2], look_free[2];  // alternating over the looks
     uint64_t v_seen[2];                  // per item parity: its drafts' V is looked through
-    uint64_t b_done, merged;             // tile B's accumulator is complete; tile A has read it
+    uint64_t both_done, merged;          // narrow: both tiles' accumulators are complete; have been read
     uint64_t item_full[2], item_empty[2];
     uint64_t fin[2];
     Item item[2];
@@ -150,8 +151,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             mbar_init(&bars.fin[x], 1);
         }
         mbar_init(&bars.q_empty, 2);
-        mbar_init(&bars.b_done, 4);
-        mbar_init(&bars.merged, 4);
+        mbar_init(&bars.both_done, 8);
+        mbar_init(&bars.merged, 8);
         bars.noted_it = -1;
         bars.abort = 0;
         fence_mbar_init();
@@ -440,7 +441,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         }
                         if (ct < kK)
                             reinterpret_cast<float*>(sm + L::kOffScale)[q * kK + ct] =
-                                reinterpret_cast<const float*>(sm + L::kOffRawScale)[raw_of(rr) * kK + ct];
+                                reinterpret_cast<const float*>(sm + L::kOffRawScale)[raw_of(rr) * kK + ct] *
+                                ((i & 1) ? 1.f : sl2);  // K's with the softmax scale
                         if (ct == 0 && !(i & 1)) bars.have[odd][(e2 >> 1) & 15] = bars.raw_have[raw_of(rr)];
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -462,7 +464,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         const uint32_t colO = tmem + lane_base + kColO + x * 128;
         const uint32_t colS = tmem + lane_base + kColS + x * 128;
         uint32_t rc = 0, a = 0;  // ring entries, key tiles of the items before
-        uint32_t n_two = 0, nseen[2] = {0, 0};
+        uint32_t nseen[2] = {0, 0};
         bool ok = true;
         auto give = [&](uint32_t slot) {  // this warp has read the scales there
             if (kCodes && lane == 0) mbar_arrive(&bars.empty[slot]);
@@ -485,7 +487,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 tc_fence_after();
                 float alpha = 1.f;
                 if (any_real) {
-                    uint32_t sr[kK];
+                    uint32_t sr[kK];  // logits; with codes in log2 units already
+                    const float sl = kCodes ? 1.f : sl2;
                     float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < kK / 32; ++c) tmem_ld32(col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sr + 32 * c));
@@ -496,10 +499,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll
                         for (int c = 0; c < kK; c += 4) {
                             const float4 f = *reinterpret_cast<const float4*>(ks + c);
-                            sr[c] = __float_as_uint(__uint_as_float(sr[c]) * f.x);
-                            sr[c + 1] = __float_as_uint(__uint_as_float(sr[c + 1]) * f.y);
-                            sr[c + 2] = __float_as_uint(__uint_as_float(sr[c + 2]) * f.z);
-                            sr[c + 3] = __float_as_uint(__uint_as_float(sr[c + 3]) * f.w);
+                            float* z = reinterpret_cast<float*>(sr) + c;
+                            mul2(z[0], z[1], f.x, f.y);
+                            mul2(z[2], z[3], f.z, f.w);
                         }
                         __syncwarp();
                         give(qk);
@@ -509,13 +511,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         float mx = max32(sr);
 #pragma unroll
                         for (int c = 1; c < kK / 32; ++c) mx = max2n(mx, max32(sr + 32 * c));
-                        alpha = st.raise(mx * sl2);
+                        alpha = st.raise(mx * sl);
                         const float nb = st.shift();
                         if (kCodes) ok = wait_warp(&bars.full[qv], use_of(e + 1), ctx, abort);  // V's scales
 #pragma unroll
                         for (int c = 0; c < kK / 32; ++c) {
                             uint32_t pk[16];
-                            exp32<false, kCodes>(sr + 32 * c, sl2, nb, 0u, vs + 32 * c, acc, pk);
+                            exp32<false, kCodes>(sr + 32 * c, sl, nb, 0u, vs + 32 * c, acc, pk);
                             tmem_st16(col + 16 * c, pk);
                         }
                     } else {
@@ -529,13 +531,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                             seen[c] = have ? (bits_to(-d0 - 1) | drafts) : 0u;
                             mx = max2n(mx, max32_masked(sr + 32 * c, seen[c]));
                         }
-                        alpha = st.raise(mx * sl2);
+                        alpha = st.raise(mx * sl);
                         const float nb = st.shift();
                         if (kCodes) ok = wait_warp(&bars.full[qv], use_of(e + 1), ctx, abort);
 #pragma unroll
                         for (int c = 0; c < kK / 32; ++c) {
                             uint32_t pk[16];
-                            exp32<true, kCodes>(sr + 32 * c, sl2, nb, seen[c], vs + 32 * c, acc, pk);
+                            exp32<true, kCodes>(sr + 32 * c, sl, nb, seen[c], vs + 32 * c, acc, pk);
                             tmem_st16(col + 16 * c, pk);
                         }
                     }
@@ -547,9 +549,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 __syncwarp();
                 give(qv);
                 if (!ok) break;
-                // Tile A reads tile B's accumulator at an item's end: B writes P, which lets the issuer
-                // start on it, only after that.
-                if (!kWide && x == 1 && k == 0 && n_two > 0) ok = wait_warp(&bars.merged, (n_two - 1) & 1, ctx, abort);
+                // Narrow: both tiles read both accumulators at an item's end.  P, which lets the issuer
+                // start on this one, comes only after that.
+                if (!kWide && k == 0 && it > 0) ok = wait_warp(&bars.merged, (it - 1) & 1, ctx, abort);
                 if (ok && k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                     const uint32_t b = a + k - 1;  // the PV before has to be done with O
                     ok = wait_warp(&bars.pv_done[x][b & 1], (b / 2) & 1, ctx, abort);
@@ -581,81 +583,95 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 if (!ok) break;
                 tc_fence_after();
             }
-            if (!kWide && x == 1) {  // tile A takes it from here
-                if (nx > 0) {
-                    ++n_two;
-                    merge[r] = make_float2(st.m, st.l);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.b_done);
-                }
-                leave_item(it);
-                continue;
-            }
-            const bool two = !kWide && m.n > 1;
+            // Narrow: the two tiles' accumulators belong to the same rows; A writes the first half of the
+            // columns of their join, B the second.
             float top = st.m, l = st.l, w_a = 1.f, w_b = 0.f;
-            if (two) {
-                ok = wait_warp(&bars.b_done, n_two++ & 1, ctx, abort);
+            if constexpr (!kWide) {
+                // (Nobody is still reading the item before: P of this one came behind it, or comes next.)
+                if (nx == 0 && it > 0) ok = wait_warp(&bars.merged, (it - 1) & 1, ctx, abort);
+                if (!ok) break;
+                merge[x * 128 + r] = make_float2(st.m, st.l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.both_done);
+                ok = wait_warp(&bars.both_done, it & 1, ctx, abort);
                 if (!ok) break;
                 tc_fence_after();
-                const float2 o = merge[r];
-                top = fmaxf(st.m, o.x);
-                w_a = st.m == -INFINITY ? 0.f : ex2(st.m - top);
-                w_b = o.x == -INFINITY ? 0.f : ex2(o.x - top);
-                l = st.l * w_a + o.y * w_b;
+                const float2 o = merge[(1 - x) * 128 + r];
+                const float m_a = x ? o.x : st.m, m_b = x ? st.m : o.x;
+                top = fmaxf(m_a, m_b);
+                w_a = m_a == -INFINITY ? 0.f : ex2(m_a - top);
+                w_b = m_b == -INFINITY ? 0.f : ex2(m_b - top);
+                l = x ? o.y * w_a + st.l * w_b : st.l * w_a + o.y * w_b;
             }
+            const bool two = !kWide && m.n > 1;
             const float inv = !m.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-            const int64_t orow = ((int64_t)m.b * s.Hkv + m.g) * s.rows + row;
+            const int64_t orow = ((int64_t)m.b * s.Hkv + m.g) * s.rows;  // of the group's row 0
             const int rt = kWide ? L::kRows : s.rows;  // rows a partial slot holds
-            const size_t slot = ((size_t)blockIdx.x * 2 + (m.tile > 0 ? 0 : 1)) * rt + (kWide ? r + 128 * x : r);
-            if (real && !m.whole) part.ml[slot] = make_float2(top, l);
+            const size_t slot = ((size_t)blockIdx.x * 2 + (m.tile > 0 ? 0 : 1)) * rt;
+            const int r0 = row - lane, s0 = kWide ? r0 - m.rt * L::kRows : r0;  // the warp's first row; in its slot
+            if (real && !m.whole && (kWide || x == 0)) part.ml[slot + s0 + lane] = make_float2(top, l);
             if (any_real) {
+                const uint32_t colA = tmem + lane_base + kColO + (kWide ? x * 128 : 0), colB = colA + 128;
+                const int c_first = kWide || x == 0 ? 0 : D / 2, c_end = kWide || x == 1 ? D : D / 2;
+                uint8_t* stage = sm + L::kOffStage + warp * 2048;
+                // 16 columns at a time, 64 bytes per row and pass (of bf16 every second time) through
+                // shared memory: four lanes then store a row's 64 bytes, whole sectors.
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(colO + c0, o);
+                for (int c0 = c_first; c0 < c_end; c0 += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(colA + c0, o);
                     if (two) {
-                        uint32_t q[32];
-                        tmem_ld32(colO + 128 + c0, q);
+                        uint32_t q[16];
+                        tmem_ld16(colB + c0, q);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             o[e] = __float_as_uint(__uint_as_float(o[e]) * w_a + __uint_as_float(q[e]) * w_b);
                     } else {
                         tmem_ld_wait();
                     }
                     if (noted) {  // rows that attend to a draft with an infinity or a NaN in V get it back
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             float y = __uint_as_float(o[e]);
                             if (notes[c0 + e] & bits) y += INFINITY;
                             if (notes[D + c0 + e] & bits) y -= INFINITY;
                             o[e] = __float_as_uint(y);
                         }
                     }
-                    if (!real) continue;
+                    auto spot = [&](int rr, int p) { return reinterpret_cast<uint4*>(stage + rr * 64 + ((p ^ ((rr >> 1) & 3)) << 4)); };
                     if (m.whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(out + orow * D + c0);
+                        uint32_t w[8];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                w[j] = pack_bf16x2(__uint_as_float(o[8 * q + 2 * j]) * inv,
-                                                   __uint_as_float(o[8 * q + 2 * j + 1]) * inv);
-                            dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int j = 0; j < 8; ++j)
+                            w[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        const int p = (c0 & 16) >> 3;
+                        *spot(lane, p) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *spot(lane, p + 1) = make_uint4(w[4], w[5], w[6], w[7]);
+                        if (p == 0) continue;
                     } else {
-                        uint4* dst = reinterpret_cast<uint4*>(part.o + slot * D + c0);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                        for (int p = 0; p < 4; ++p) *spot(lane, p) = make_uint4(o[4 * p], o[4 * p + 1], o[4 * p + 2], o[4 * p + 3]);
                     }
+                    __syncwarp();
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        const int rr = 8 * p + (lane >> 2);
+                        const uint4 v = *spot(rr, lane & 3);
+                        if (r0 + rr < s.rows) {
+                            if (m.whole)
+                                *reinterpret_cast<uint4*>(out + (orow + r0 + rr) * D + (c0 - 16) + 8 * (lane & 3)) = v;
+                            else
+                                *reinterpret_cast<uint4*>(part.o + (slot + s0 + rr) * D + c0 + 4 * (lane & 3)) = v;
+                        }
+                    }
+                    __syncwarp();
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (two && lane == 0) mbar_arrive(&bars.merged);
+            if (!kWide && lane == 0) mbar_arrive(&bars.merged);
             leave_item(it);
         }
     }
