@@ -100,6 +100,44 @@ __device__ __forceinline__ uint2 codes_to_bf16(uint32_t c) {
         return make_uint2(code_pair<F>(__byte_perm(c, 0u, 0x1404)), code_pair<F>(__byte_perm(c, 0u, 0x3424)));
 }
 
+// Two codes as an fp16 pair, exactly.  u holds a code in each low byte of 16 bits: for Int8 offset by 128
+// (xor 0x80) below the byte 0x64, which makes 1024 + 128 + code; for E4M3 both codes are in the low 16 bits.
+template <KvFormat F>
+__device__ __forceinline__ uint32_t code_pair_f16(uint32_t u) {
+    if constexpr (F == KvFormat::Int8) {
+        const uint32_t k = 0x64806480u;  // 1152
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&k));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    } else {
+        const __half2 d(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(u & 0xffffu), __NV_E4M3));
+        return *reinterpret_cast<const uint32_t*>(&d);
+    }
+}
+// fp16 pairs of four codes in memory order.
+template <KvFormat F>
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t c) {
+    if constexpr (F == KvFormat::Int8) {
+        c ^= 0x80808080u;
+        return make_uint2(code_pair_f16<F>(__byte_perm(c, 0x64646464u, 0x4140)),
+                          code_pair_f16<F>(__byte_perm(c, 0x64646464u, 0x4342)));
+    } else {
+        return make_uint2(code_pair_f16<F>(c), code_pair_f16<F>(c >> 16));
+    }
+}
+// Codes of two rows a (bytes 0, 1) and b (bytes 2, 3), as a transposing load leaves them: fp16 pairs
+// (byte 0, byte 2) and (byte 1, byte 3).
+template <KvFormat F>
+__device__ __forceinline__ uint2 crossed_to_f16(uint32_t c) {
+    if constexpr (F == KvFormat::Int8) {
+        c ^= 0x80808080u;
+        return make_uint2(code_pair_f16<F>(__byte_perm(c, 0x64646464u, 0x4240)),
+                          code_pair_f16<F>(__byte_perm(c, 0x64646464u, 0x4341)));
+    } else {
+        const uint32_t a = code_pair_f16<F>(c), b = code_pair_f16<F>(c >> 16);
+        return make_uint2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    }
+}
+
 // ---------------------------------------------------------------- packed sequences
 // Rows cu[b] .. cu[b + 1] of a packed tensor belong to sequence b.  A pair of offsets that does not
 // lie in order inside [0, total] counts as an empty sequence and sets *bad.

@@ -27,6 +27,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // Maxima that pass NaN on.
 __device__ __forceinline__ float max2n(float a, float b) {
     float d;
@@ -65,6 +70,17 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, co
             return false;
         }
     }
+    return true;
+}
+// The same for a warp that no other one waits for.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, const DevCtx& ctx) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_long(bar, parity))
+        if (globaltimer_ns() - t0 > ctx.wait_limit_ns) {
+            flag(ctx, kStatusTimeout);
+            return false;
+        }
     return true;
 }
 // The same with one outcome for the whole (converged) warp.

@@ -15,8 +15,15 @@
 // different banks under the 128-byte swizzle; P's columns meet V's rows in the same order.  V comes
 // transposed (ldmatrix): of codes, two neighbouring columns at a time, split by byte.
 //
-// 8-bit scales, hidden positions, infinities and NaN: as in the tensor-core kernel (tree_tc.cu).  The
-// warps' accumulators are joined in shared memory at an item's end.
+// Codes are multiplied as fp16, which they are exactly and which takes two to three instructions a
+// pair where bf16 takes five (the conversion is half of the kernel's instructions).  Q's rows are
+// brought to it by a power of two that puts their largest value in [1, 2); what falls below fp16's
+// smallest step then is 2^-25 of that value.  P has no such bound, as it carries the scales of V's
+// rows: the weight of key j in O is 2^(y_j + log2 sv_j - M) with a running maximum M of its own
+// exponent, the one in the row's sum 2^(y_j - m) as ever, and O is brought to m at the item's end.
+//
+// Hidden positions, infinities and NaN: as in the tensor-core kernel (tree_tc.cu).  The warps'
+// accumulators are joined in shared memory at an item's end.
 #include <type_traits>
 
 #include "decode_common.cuh"
@@ -44,8 +51,9 @@ struct Layout {
     static constexpr int kWarps = kRowBytes > 128 ? 6 : 12;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kStage = 2 * kTile;                             // a warp's K and V
-    static constexpr int kOffScale = kWarps * kStage;                    // [warp][k, v][64]
-    static constexpr int kOffNotes = kOffScale + (kCodes ? kWarps * 2 * kPage * 4 : 0);
+    static constexpr int kOffScale = kWarps * kStage;                    // [warp][k, v, log2 v][64]
+    static constexpr int kOffQ = kOffScale + (kCodes ? kWarps * 3 * kPage * 4 : 0);  // [step][lane], 16 bytes
+    static constexpr int kOffNotes = kOffQ + (D / 16) * 512;
     static constexpr int kOffMl = kOffNotes + (kCodes ? 0 : 2 * D * 8);  // [warp][16] (maximum, sum)
     static constexpr int kOffBars = kOffMl + kWarps * kRows * 8;
     static constexpr int kBytes = kOffBars + kWarps * 2 * 8;
@@ -82,8 +90,9 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int g = lane >> 2, t = lane & 3;    // fragment row (and row + 8), column pair
     uint8_t* K = sm + warp * L::kStage;
     uint8_t* V = K + L::kTile;
-    float* ksc = reinterpret_cast<float*>(sm + L::kOffScale) + warp * 2 * kPage;
+    float* ksc = reinterpret_cast<float*>(sm + L::kOffScale) + warp * 3 * kPage;
     float* vsc = ksc + kPage;
+    float* vlg = vsc + kPage;
     unsigned long long* notes = reinterpret_cast<unsigned long long*>(sm + L::kOffNotes);
     float2* ml = reinterpret_cast<float2*>(sm + L::kOffMl);
     uint64_t* kbar = reinterpret_cast<uint64_t*>(sm + L::kOffBars) + warp * 2;
@@ -160,8 +169,11 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         load(id, false);
 
         // Q's fragments and the rows' draft masks.
-        uint32_t qa[kSteps][4];
         uint64_t bits[2];
+        float sl[2] = {sl2, sl2};  // per row: from S to log2 units
+        uint4* qf = reinterpret_cast<uint4*>(sm + L::kOffQ) + lane;
+        {
+        uint32_t qa[kSteps][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int r = g + 8 * h;
@@ -176,13 +188,40 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 qa[st][h] = u.x;
                 qa[st][2 + h] = u.y;
             }
+            if constexpr (kCodes) {  // to fp16, the largest value in [1, 2)
+                uint32_t m = 0u;
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st)
+                    m = __vmaxu2(m, __vmaxu2(qa[st][h] & 0x7fff7fffu, qa[st][2 + h] & 0x7fff7fffu));
+                m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                int ex = (int)(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent
+                if (ex == 255) ex = 127;                         // an infinity or a NaN stays what it is
+                ex = min(max(ex, 1), 253);
+                const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+                sl[h] = sl2 * __uint_as_float((uint32_t)ex << 23);
+                auto half2 = [&](uint32_t w) {
+                    const __half2 v = __floats2half2_rn(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
+                    return *reinterpret_cast<const uint32_t*>(&v);
+                };
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st) {
+                    qa[st][h] = half2(qa[st][h]);
+                    qa[st][2 + h] = half2(qa[st][2 + h]);
+                }
+            }
+        }
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)  // every warp has them all; one puts them down
+            if (st % L::kWarps == warp) qf[st * 32] = make_uint4(qa[st][0], qa[st][1], qa[st][2], qa[st][3]);
         }
         if constexpr (!kCodes) {
             if (tid == 0) noted = 0;
             for (int e = tid; e < 2 * D; e += L::kThreads) notes[e] = 0ull;
-            __syncthreads();
         }
+        __syncthreads();
         RowState st[2];
+        float top_v[2] = {-INFINITY, -INFINITY};  // M
         float o[D / 8][4];
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
@@ -198,26 +237,36 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 load(id, false);
                 continue;
             }
-            if (!dead && !__all_sync(0xffffffffu, mbar_wait(kbar, (nk - 1) & 1, ctx))) dead = true;
+            if (!dead && !__all_sync(0xffffffffu, wait_long(kbar, (nk - 1) & 1, ctx))) dead = true;
             if (dead) break;
             float sc[8][4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-                const int r = 8 * j + key_of<L>(g);
+            for (int j = 0; j < 8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
 #pragma unroll
-                for (int p = 0; p < kPieces / 4; ++p) {
-                    const uint4 u = ld16(piece<L>(K, r, 4 * p + t));
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            for (int p = 0; p < kPieces / 4; ++p) {
+                constexpr int kN = kPer / 4;  // steps that 16 bytes make
+                uint32_t qa[kN][4];
+#pragma unroll
+                for (int x = 0; x < kN; ++x) {
+                    const uint4 u = qf[(kN * p + x) * 32];
+                    qa[x][0] = u.x;
+                    qa[x][1] = u.y;
+                    qa[x][2] = u.z;
+                    qa[x][3] = u.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint4 u = ld16(piece<L>(K, 8 * j + key_of<L>(g), 4 * p + t));
                     if constexpr (kCodes) {
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
-                            const uint2 b = codes_to_bf16<F>(w[x]);
-                            mma16816(sc[j], qa[4 * p + x], {b.x, b.y});
+                            const uint2 b = codes_to_f16<F>(w[x]);
+                            mma16816_f16(sc[j], qa[x], {b.x, b.y});
                         }
                     } else {
-                        mma16816(sc[j], qa[2 * p], {w[0], w[1]});
-                        mma16816(sc[j], qa[2 * p + 1], {w[2], w[3]});
+                        mma16816(sc[j], qa[0], {u.x, u.y});
+                        mma16816(sc[j], qa[1], {u.z, u.w});
                     }
                 }
             }
@@ -250,24 +299,69 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         }
                 }
             }
-            float alpha[2], nb[2];
+            [[maybe_unused]] float alpha[2], nb[2], nv_[2] = {0.f, 0.f};  // nb, nv_: added to the exponents of l's and of O's weights
+            if constexpr (!kCodes) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float mx = -INFINITY;
+                for (int h = 0; h < 2; ++h) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if constexpr (!tail) {
+                            mx = max3n(mx, sc[j][2 * h], sc[j][2 * h + 1]);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                if ((seen[h] >> (2 * j + x)) & 1u) mx = max2n(mx, sc[j][2 * h + x]);
+                        }
+                    }
+                    mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    alpha[h] = st[h].raise(mx * sl2);
+                    nb[h] = st[h].shift();
+                }
+            }
+            if (!__all_sync(0xffffffffu, wait_long(vbar, (nv - 1) & 1, ctx))) {
+                dead = true;
+                return false;
+            }
+            if constexpr (kCodes) {
+                vlg[lane] = lg2(vsc[lane]);
+                vlg[lane + 32] = lg2(vsc[lane + 32]);
+                __syncwarp();
+                float mx[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    if constexpr (!tail) {
-                        mx = max3n(mx, sc[j][2 * h], sc[j][2 * h + 1]);
-                    } else {
+                    const float va = vlg[8 * j + key_of<L>(2 * t)], vb = vlg[8 * j + key_of<L>(2 * t + 1)];
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            if ((seen[h] >> (2 * j + x)) & 1u) mx = max2n(mx, sc[j][2 * h + x]);
+                    for (int h = 0; h < 2; ++h) {
+                        const float y0 = sc[j][2 * h] *= sl[h], y1 = sc[j][2 * h + 1] *= sl[h];
+                        if (!tail || ((seen[h] >> (2 * j)) & 1u)) {
+                            mx[h] = max2n(mx[h], y0);
+                            mv[h] = max2n(mv[h], y0 + va);
+                        }
+                        if (!tail || ((seen[h] >> (2 * j + 1)) & 1u)) {
+                            mx[h] = max2n(mx[h], y1);
+                            mv[h] = max2n(mv[h], y1 + vb);
+                        }
                     }
                 }
-                mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                alpha[h] = st[h].raise(mx * sl2);
-                nb[h] = st[h].shift();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) {
+                        mx[h] = max2n(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], o));
+                        mv[h] = max2n(mv[h], __shfl_xor_sync(0xffffffffu, mv[h], o));
+                    }
+                    (void)st[h].raise(mx[h]);
+                    nb[h] = st[h].shift();
+                    alpha[h] = 1.f;  // of O
+                    if (mv[h] > top_v[h] + kGrow) {
+                        if (top_v[h] != -INFINITY) alpha[h] = ex2(top_v[h] - mv[h]);
+                        top_v[h] = mv[h];
+                    }
+                    if (!(mv[h] <= 3.402823466e38f)) st[h].l = __uint_as_float(0x7fffffffu);
+                    nv_[h] = top_v[h] == -INFINITY ? 0.f : -top_v[h];
+                }
             }
             if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
@@ -277,10 +371,6 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     o[e][2] *= alpha[1];
                     o[e][3] *= alpha[1];
                 }
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait(vbar, (nv - 1) & 1, ctx))) {
-                dead = true;
-                return false;
             }
             if constexpr (!kCodes) {
                 if constexpr (tail) {  // V's rows that not every row sees: see tree_tc.cu
@@ -311,21 +401,24 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     const int j = 2 * jj + y;
-                    [[maybe_unused]] float va = 1.f, vb = 1.f;
+                    [[maybe_unused]] float va, vb;
                     if constexpr (kCodes) {
-                        va = vsc[8 * j + key_of<L>(2 * t)];
-                        vb = vsc[8 * j + key_of<L>(2 * t + 1)];
+                        va = vlg[8 * j + key_of<L>(2 * t)];
+                        vb = vlg[8 * j + key_of<L>(2 * t + 1)];
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float p0 = ex2(fmaf(sc[j][2 * h], sl2, nb[h])), p1 = ex2(fmaf(sc[j][2 * h + 1], sl2, nb[h]));
                         const bool s0 = !tail || ((seen[h] >> (2 * j)) & 1u), s1 = !tail || ((seen[h] >> (2 * j + 1)) & 1u);
-                        st[h].l += (s0 ? p0 : 0.f) + (s1 ? p1 : 0.f);
+                        const float x0 = sc[j][2 * h], x1 = sc[j][2 * h + 1];
                         if constexpr (kCodes) {
-                            p0 *= va;
-                            p1 *= vb;
+                            st[h].l += (s0 ? ex2(x0 + nb[h]) : 0.f) + (s1 ? ex2(x1 + nb[h]) : 0.f);
+                            const __half2 w = __floats2half2_rn(s0 ? ex2(x0 + (va + nv_[h])) : 0.f, s1 ? ex2(x1 + (vb + nv_[h])) : 0.f);
+                            pa[2 * y + h] = *reinterpret_cast<const uint32_t*>(&w);
+                        } else {
+                            const float p0 = ex2(fmaf(x0, sl2, nb[h])), p1 = ex2(fmaf(x1, sl2, nb[h]));
+                            st[h].l += (s0 ? p0 : 0.f) + (s1 ? p1 : 0.f);
+                            pa[2 * y + h] = pack_bf16x2(s0 ? p0 : 0.f, s1 ? p1 : 0.f);
                         }
-                        pa[2 * y + h] = pack_bf16x2(s0 ? p0 : 0.f, s1 ? p1 : 0.f);
                     }
                 }
                 // lanes 8 m .. 8 m + 7 address matrix m: 8 keys of tile 2 jj + (m & 1), piece p + (m >> 1)
@@ -337,12 +430,10 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const uint32_t a = u[2 * y], b = u[2 * y + 1];
-                        if constexpr (F == KvFormat::Int8) {
-                            mma16816(o[2 * (p + y)], pa, {code_pair<F>(__byte_perm(a, 0u, 0x4240)), code_pair<F>(__byte_perm(b, 0u, 0x4240))});
-                            mma16816(o[2 * (p + y) + 1], pa, {code_pair<F>(__byte_perm(a, 0u, 0x4341)), code_pair<F>(__byte_perm(b, 0u, 0x4341))});
-                        } else if constexpr (F == KvFormat::E4M3) {
-                            mma16816(o[2 * (p + y)], pa, {code_pair<F>(__byte_perm(a, 0u, 0x2404)), code_pair<F>(__byte_perm(b, 0u, 0x2404))});
-                            mma16816(o[2 * (p + y) + 1], pa, {code_pair<F>(__byte_perm(a, 0u, 0x3414)), code_pair<F>(__byte_perm(b, 0u, 0x3414))});
+                        if constexpr (kCodes) {
+                            const uint2 fa = crossed_to_f16<F>(a), fb = crossed_to_f16<F>(b);
+                            mma16816_f16(o[2 * (p + y)], pa, {fa.x, fb.x});
+                            mma16816_f16(o[2 * (p + y) + 1], pa, {fa.y, fb.y});
                         } else {
                             mma16816(o[p + y], pa, {a, b});
                         }
@@ -366,6 +457,14 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             l += __shfl_xor_sync(0xffffffffu, l, 2);
             if (t == 0) ml[warp * kRows + g + 8 * h] = make_float2(st[h].m, l);
             float* dst = reinterpret_cast<float*>(K) + (g + 8 * h) * D;
+            if constexpr (kCodes) {  // O from M to m
+                const float f = top_v[h] == -INFINITY ? 0.f : ex2(top_v[h] - (st[h].m == -INFINITY ? 0.f : st[h].m));
+#pragma unroll
+                for (int e = 0; e < D / 8; ++e) {
+                    o[e][2 * h] *= f;
+                    o[e][2 * h + 1] *= f;
+                }
+            }
             if (n_my > 0 && !dead) {
                 if constexpr (kCodes) {  // tiles 2 p and 2 p + 1: columns 16 p + 4 t + 0, 2 and 1, 3
 #pragma unroll
