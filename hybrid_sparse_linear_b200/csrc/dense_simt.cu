@@ -3,9 +3,10 @@
 //
 // One block takes 64 query rows and walks 64-key tiles with the running maximum and sum of the
 // softmax in registers: S = Q K^T as 4 x 4 values per thread, P through shared memory, O += P V
-// with 4 x D/16 sums per thread.  Per tile 2 * 64 * 64 * D multiply-adds against 2 * 64 * D loads:
-// bound by the fp32 FMA units once more than one block runs per SM (84 KB each, two per SM).
-// K and V of a tile take turns in one buffer, which is what lets two blocks share an SM.
+// with 4 x D/16 sums per thread.  Per tile 2 * 64 * 64 * D multiply-adds against 2 * 64 * D loads: the
+// fp32 FMA units are the bound once the loads are out of the way, so V's tile is on its way into
+// registers while S is formed and the next K's while P V is (loads at the point of use: 150 us for the
+// 2049 ragged tokens of eight heads of 64 that take XX us).
 //
 // Masked positions are left out by selection, never by adding a large negative number or by
 // multiplying with zero: a hidden key or value may hold an infinity or a NaN without touching the
@@ -28,7 +29,10 @@ constexpr int kPad0 = 1;    // beginning an item costs about a tile
 constexpr float kHidden = -1.f;  // P of a position its row does not see (probabilities are >= 0)
 
 template <int D>
-constexpr int smem_floats() { return 2 * kRows * (D + kPad) + kRows * (kKeys + kPad); }
+constexpr int smem_floats() { return (kRows + 2 * kKeys) * (D + kPad) + kRows * (kKeys + kPad); }
+// Blocks per SM that its shared memory holds.
+template <int D>
+constexpr int blocks_per_sm() { return D == 64 ? 2 : 1; }
 
 // The state of 64 query rows in 256 threads: thread (ty, tx) = (tid / 16, tid % 16) holds rows
 // 4 ty .. 4 ty + 3 and of each the output columns 64 j + 4 tx .. + 3.
@@ -47,21 +51,43 @@ struct Rows {
     }
 };
 
-// One key tile.  load(r, c) gives 4 consecutive floats of key (value) row r; seen(row, key) says
+// A tile's K or V on its way: 4 consecutive floats of row r per thread and step, by load(r, c).
+template <int D>
+struct Fetch {
+    static constexpr int kN = kKeys * (D / 4) / kThreads;
+    float4 x[kN];
+    template <class Load>
+    __device__ __forceinline__ void get(Load load) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            x[i] = load(e / (D / 4), (e % (D / 4)) * 4);
+        }
+    }
+    __device__ __forceinline__ void put(float* sm) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            *reinterpret_cast<float4*>(sm + e / (D / 4) * (D + kPad) + (e % (D / 4)) * 4) = x[i];
+        }
+    }
+};
+
+// One key tile; k holds its K.  load_v loads its V, next_k the next tile's K into k; seen(row, key) says
 // whether the row attends to the tile's key; masked: whether any position may be hidden.
-template <int D, class LoadK, class LoadV, class Seen>
-__device__ __forceinline__ void attend_tile(Rows<D>& st, float* sm, float sl2, bool masked,
-                                            LoadK load_k, LoadV load_v, Seen seen) {
+template <int D, class LoadV, class NextK, class Seen>
+__device__ __forceinline__ void attend_tile(Rows<D>& st, float* sm, float sl2, bool masked, Fetch<D>& k,
+                                            LoadV load_v, NextK next_k, Seen seen) {
     constexpr int kLd = D + kPad, kLp = kKeys + kPad;
     float* Q = sm;
-    float* KV = sm + kRows * kLd;
-    float* P = KV + kKeys * kLd;
+    float* K = sm + kRows * kLd;
+    float* V = K + kKeys * kLd;
+    float* P = V + kKeys * kLd;
     const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
-        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
-        *reinterpret_cast<float4*>(KV + r * kLd + c) = load_k(r, c);
-    }
+    k.put(K);  // (S of the tile before is done with it: a barrier lies between)
     __syncthreads();
+    Fetch<D> v;
+    v.get(load_v);
     float s[4][4] = {};
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
@@ -69,7 +95,7 @@ __device__ __forceinline__ void attend_tile(Rows<D>& st, float* sm, float sl2, b
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(Q + (ty * 4 + i) * kLd + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(KV + (tx + 16 * j) * kLd + c);
+        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(K + (tx + 16 * j) * kLd + c);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -105,12 +131,9 @@ __device__ __forceinline__ void attend_tile(Rows<D>& st, float* sm, float sl2, b
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) st.acc[i][c] *= alpha;
     }
-    __syncthreads();  // S is done with K
-    for (int e = tid; e < kKeys * (D / 4); e += kThreads) {
-        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
-        *reinterpret_cast<float4*>(KV + r * kLd + c) = load_v(r, c);
-    }
+    v.put(V);
     __syncthreads();
+    next_k(k);
     auto pv = [&](auto hide) {
 #pragma unroll 2
         for (int k = 0; k < kKeys; k += 4) {
@@ -121,7 +144,7 @@ __device__ __forceinline__ void attend_tile(Rows<D>& st, float* sm, float sl2, b
             for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j) {
-                    const float4 v = *reinterpret_cast<const float4*>(KV + (k + kk) * kLd + 64 * j + 4 * tx);
+                    const float4 v = *reinterpret_cast<const float4*>(V + (k + kk) * kLd + 64 * j + 4 * tx);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
@@ -136,7 +159,6 @@ __device__ __forceinline__ void attend_tile(Rows<D>& st, float* sm, float sl2, b
     };
     if (masked) pv(std::true_type{});
     else pv(std::false_type{});
-    __syncthreads();  // the next tile writes KV and P
 }
 
 __device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
@@ -158,7 +180,7 @@ __device__ __forceinline__ float4 kv_load4(const void* p, const float* scale, in
 // Block = (64 consecutive tokens of one sequence, one query head); blockIdx.x counts the tiles of
 // all sequences, an upper bound of which the host launches.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<D>())
 packed_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                    const int32_t* __restrict__ cu, float* __restrict__ out, int B, int H, int Hkv,
                    int total, float sl2, DevCtx ctx) {
@@ -186,14 +208,17 @@ packed_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, con
     }
     Rows<D> st;
     st.clear();
+    auto load = [&](const float* base, int j, int c) {  // key or value j
+        return j < t.len ? load4(base + (int64_t)j * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    Fetch<D> kf;
+    kf.get([&](int r, int c) { return load(kb, r, c); });
     for (int k0 = 0; k0 <= t.first; k0 += kKeys) {
-        const bool masked = k0 + kKeys > t.first;
-        const int n_keys = min(kKeys, t.len - k0);
-        auto load = [&](const float* base, int r, int c) {
-            return r < n_keys ? load4(base + (int64_t)(k0 + r) * D + c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-        attend_tile<D>(st, sm, sl2, masked, [&](int r, int c) { return load(kb, r, c); },
-                       [&](int r, int c) { return load(vb, r, c); },
+        attend_tile<D>(st, sm, sl2, k0 + kKeys > t.first, kf,
+                       [&](int r, int c) { return load(vb, k0 + r, c); },
+                       [&](Fetch<D>& f) {
+                           if (k0 + kKeys <= t.first) f.get([&](int r, int c) { return load(kb, k0 + kKeys + r, c); });
+                       },
                        [&](int row, int key) { return k0 + key <= t.first + row; });
     }
     const int ty = tid >> 4, tx = tid & 15;
@@ -212,7 +237,7 @@ packed_simt_kernel(const float* __restrict__ q, const float* __restrict__ k, con
 
 // ---------------------------------------------------------------- drafted tokens, paged cache
 template <int D, KvFormat F>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm<D>())
 tree_simt_kernel(const float* __restrict__ q, KvPages pages, const uint64_t* __restrict__ masks,
                  float* __restrict__ out, tree::Shape s, tree::Partials part, float sl2, DevCtx ctx) {
     extern __shared__ __align__(16) float sm[];
@@ -247,25 +272,29 @@ tree_simt_kernel(const float* __restrict__ q, KvPages pages, const uint64_t* __r
         __syncthreads();
         Rows<D> st;
         st.clear();
+        // A page the table does not hold: its keys are left out.
+        auto page_at = [&](int tl) { return page_of(pages, c.b, tl); };
+        auto load = [&](const void* p, const float* sc, int page, int tl, int r, int col) {
+            const bool have = page >= 0 && tl * kKeys + r < c.ctx + s.T;
+            return have ? kv_load4<F>(p, sc, ((int64_t)page * s.Hkv + c.g) * kKeys + r, D, col)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        int page = page_at(t0);
+        Fetch<D> kf;
+        kf.get([&](int r, int col) { return load(pages.k, pages.k_scale, page, t0, r, col); });
         for (int t = t0; t < t0 + n; ++t) {
-            const int k0 = t * kKeys;
-            const int page = page_of(pages, c.b, t);
-            if (page < 0) {  // a page the table does not hold: its keys are left out
-                if (tid == 0) flag(ctx, kStatusBounds);
-                continue;
-            }
-            const int n_keys = min(kKeys, c.ctx + s.T - k0);
-            const int64_t base = ((int64_t)page * s.Hkv + c.g) * kKeys;
-            auto load = [&](const void* p, const float* sc, int r, int col) {
-                return r < n_keys ? kv_load4<F>(p, sc, base + r, D, col) : make_float4(0.f, 0.f, 0.f, 0.f);
-            };
-            attend_tile<D>(st, sm, sl2, k0 + kKeys > c.ctx,
-                           [&](int r, int col) { return load(pages.k, pages.k_scale, r, col); },
-                           [&](int r, int col) { return load(pages.v, pages.v_scale, r, col); },
+            if (page < 0 && tid == 0) flag(ctx, kStatusBounds);
+            const int next = t + 1 < t0 + n ? page_at(t + 1) : -1, k0 = t * kKeys;
+            attend_tile<D>(st, sm, sl2, k0 + kKeys > c.ctx || page < 0, kf,
+                           [&](int r, int col) { return load(pages.v, pages.v_scale, page, t, r, col); },
+                           [&](Fetch<D>& f) {
+                               f.get([&](int r, int col) { return load(pages.k, pages.k_scale, next, t + 1, r, col); });
+                           },
                            [&](int row, int key) {
                                const int j = k0 + key - c.ctx;  // draft number
-                               return j < 0 || (j < s.T && ((bits[row] >> j) & 1ull));
+                               return page >= 0 && (j < 0 || (j < s.T && ((bits[row] >> j) & 1ull)));
                            });
+            page = next;
         }
         const bool whole = n == c.n_tiles;
         const size_t slot = ((size_t)blockIdx.x * 2 + (t0 > 0 ? 0 : 1)) * min(s.rows, kRows);
@@ -301,14 +330,14 @@ cudaError_t packed_simt(const void* q, const void* k, const void* v, const int32
 
 // A partial slot holds a row tile, or the group's rows where they are fewer.
 int slot_rows(int rows) { return rows < kRows ? rows : kRows; }
-int tree_ctas() { return 2 * device_sm_count(); }
+int tree_ctas(int d) { return (d == 64 ? blocks_per_sm<64>() : blocks_per_sm<128>()) * device_sm_count(); }
 
 template <int D, KvFormat F>
 cudaError_t tree_simt(const void* q, const KvPages& pages, const uint64_t* masks, void* o,
                       const tree::Shape& s, void* ws, float scale, cudaStream_t st, DevCtx ctx) {
     constexpr int bytes = smem_floats<D>() * 4;
     if (cudaError_t e = ensure_smem<tree_simt_kernel<D, F>>(bytes); e != cudaSuccess) return e;
-    const int n_cta = tree_ctas();
+    const int n_cta = tree_ctas(D);
     const tree::Partials part = tree::partials_at(ws, n_cta, slot_rows(s.rows));
     tree_simt_kernel<D, F><<<n_cta, kThreads, bytes, st>>>(
         static_cast<const float*>(q), pages, masks, static_cast<float*>(o), s, part,
@@ -319,7 +348,7 @@ cudaError_t tree_simt(const void* q, const KvPages& pages, const uint64_t* masks
 
 }  // namespace
 
-size_t tree_simt_workspace(int rows, int d) { return tree::partial_bytes(tree_ctas(), slot_rows(rows), d); }
+size_t tree_simt_workspace(int rows, int d) { return tree::partial_bytes(tree_ctas(d), slot_rows(rows), d); }
 
 cudaError_t launch_packed_simt(const void* q, const void* k, const void* v, const int32_t* cu, void* o,
                                int B, int H, int Hkv, int total, int d, float scale, cudaStream_t st,
