@@ -7,7 +7,6 @@ library is missing this module fails to import.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -505,19 +504,16 @@ def sparse_decode_paged(q, k_pages, v_pages, page_table, kbar, pos, max_pos, top
 # ----------------------------------------------------------------------------------------------
 # Dense serving path: packed prompts, the paged cache, and new or drafted tokens over it
 
-_NO_SWITCH = contextlib.nullcontext()
-
-
-def _on(dev, stream):
-    """Context in which a call on a device allocates and launches: the given stream (whose pool then
-    owns what the call allocates), else the device's current stream."""
+def _switch(dev, stream):
+    """Where a call on a device has to switch first, the context for it: to the given stream (whose
+    pool then owns what the call allocates), or to the tensors' device.  None: nothing to switch."""
     if stream is not None:
         if stream.device != dev:
             raise ValueError(f"stream on {stream.device}, tensors on {dev}")
         return torch.cuda.stream(stream)
     if dev.index != torch.cuda.current_device():
         return torch.cuda.stream(torch.cuda.current_stream(dev))
-    return _NO_SWITCH
+    return None
 
 
 # The current stream of a device as an integer; torch.cuda.current_stream() builds a Stream object
@@ -534,11 +530,18 @@ def _fit(t, name, shape, dtype, dev):
         raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
 
 
+def _lies(t, name, dtype, dev):
+    """_fit for a tensor of any shape."""
+    if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _fit(t, name, t.shape, dtype, dev)
+
+
 def _offsets_batch(cu_seqlens, dev):
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+    n = cu_seqlens.numel()
+    if n < 1 or cu_seqlens.dim() != 1:
         raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, expected (B + 1,)")
-    _fit(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
-    return cu_seqlens.shape[0] - 1
+    _lies(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    return n - 1
 
 
 _KV_FORMATS = {torch.int8: KV_INT8, torch.float8_e4m3fn: KV_E4M3}
@@ -557,11 +560,11 @@ def _pool(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype, dev):
     shape, kind = k_pages.shape, k_pages.dtype
     if len(shape) != 4 or shape[2] != 64:
         raise ValueError(f"k_pages has shape {tuple(shape)}, expected (n_pages, Hkv, 64, d)")
-    _fit(k_pages, "k_pages", shape, kind, dev)
+    _lies(k_pages, "k_pages", kind, dev)
     _fit(v_pages, "v_pages", shape, kind, dev)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({B}, max_pages)")
-    _fit(page_table, "page_table", page_table.shape, torch.int32, dev)
+    _lies(page_table, "page_table", torch.int32, dev)
     fmt = _KV_FORMATS.get(kind, KV_SAME)
     if fmt == KV_SAME:
         if kind != dtype:
@@ -586,19 +589,21 @@ def packed_prefill(q, k, v, cu_seqlens, o=None, scale=0.0, stream=None):
     (H, total, d), dtype, dev = q.shape, q.dtype, q.device
     if k.dim() != 3 or k.shape[1:] != (total, d):
         raise ValueError(f"k has shape {tuple(k.shape)}, expected (Hkv, {total}, {d})")
-    _fit(k, "k", k.shape, dtype, dev)
+    _lies(k, "k", dtype, dev)
     _fit(v, "v", k.shape, dtype, dev)
     B = _offsets_batch(cu_seqlens, dev)
     code = _code(dtype)
-    with _on(dev, stream):
-        if o is None:
-            o = torch.empty_like(q)
-        else:
-            _fit(o, "o", q.shape, dtype, dev)
-        r = _lib.sala_packed_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
-                                     o.data_ptr(), B, H, k.shape[0], total, d, scale, code,
-                                     _raw_stream(dev.index))
-    _check(r, "sala_packed_prefill")
+    other = _switch(dev, stream)
+    if other is not None:
+        with other:
+            return packed_prefill(q, k, v, cu_seqlens, o, scale)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _fit(o, "o", q.shape, dtype, dev)
+    _check(_lib.sala_packed_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
+                                    o.data_ptr(), B, H, k.shape[0], total, d, scale, code,
+                                    _raw_stream(dev.index)), "sala_packed_prefill")
     return o
 
 
@@ -619,12 +624,14 @@ def kv_write(k, v, cu_seqlens, pos, page_table, k_pages, v_pages, k_scale=None, 
     if Hk != Hkv or dk != d:
         raise ValueError(f"k has shape {tuple(k.shape)}, the pages hold ({Hkv}, tokens, {d})")
     code = _code(dtype)
-    with _on(dev, stream):
-        r = _lib.sala_kv_write(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), pos.data_ptr(),
-                               page_table.data_ptr(), page_table.shape[1], k_pages.data_ptr(),
-                               v_pages.data_ptr(), ks, vs, n_pages, B, Hkv, total, d, 64, fmt, code,
-                               _raw_stream(dev.index))
-    _check(r, "sala_kv_write")
+    other = _switch(dev, stream)
+    if other is not None:
+        with other:
+            return kv_write(k, v, cu_seqlens, pos, page_table, k_pages, v_pages, k_scale, v_scale)
+    _check(_lib.sala_kv_write(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), pos.data_ptr(),
+                              page_table.data_ptr(), page_table.shape[1], k_pages.data_ptr(),
+                              v_pages.data_ptr(), ks, vs, n_pages, B, Hkv, total, d, 64, fmt, code,
+                              _raw_stream(dev.index)), "sala_kv_write")
 
 
 def kv_read(k_pages, v_pages, page_table, cu_seqlens, pos, total, dtype, k_scale=None, v_scale=None,
@@ -640,21 +647,24 @@ def kv_read(k_pages, v_pages, page_table, cu_seqlens, pos, total, dtype, k_scale
     if not 0 <= total < 1 << 31:
         raise ValueError(f"total {total} outside [0, 2^31)")
     code = _code(dtype)
+    other = _switch(dev, stream)
+    if other is not None:
+        with other:
+            return kv_read(k_pages, v_pages, page_table, cu_seqlens, pos, total, dtype, k_scale, v_scale,
+                           k, v)
     shape = (Hkv, total, d)
-    with _on(dev, stream):
-        if k is None:
-            k = torch.empty(shape, dtype=dtype, device=dev)
-        else:
-            _fit(k, "k", shape, dtype, dev)
-        if v is None:
-            v = torch.empty_like(k)
-        else:
-            _fit(v, "v", shape, dtype, dev)
-        r = _lib.sala_kv_read(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, n_pages,
-                              page_table.data_ptr(), page_table.shape[1], cu_seqlens.data_ptr(),
-                              pos.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, total, d, 64, fmt,
-                              code, _raw_stream(dev.index))
-    _check(r, "sala_kv_read")
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=dev)
+    else:
+        _fit(k, "k", shape, dtype, dev)
+    if v is None:
+        v = torch.empty_like(k)
+    else:
+        _fit(v, "v", shape, dtype, dev)
+    _check(_lib.sala_kv_read(k_pages.data_ptr(), v_pages.data_ptr(), ks, vs, n_pages,
+                             page_table.data_ptr(), page_table.shape[1], cu_seqlens.data_ptr(),
+                             pos.data_ptr(), k.data_ptr(), v.data_ptr(), B, Hkv, total, d, 64, fmt, code,
+                             _raw_stream(dev.index)), "sala_kv_read")
     return k, v
 
 
@@ -680,22 +690,25 @@ def tree_decode_paged(q, k_pages, v_pages, page_table, ctx, max_ctx, tree, k_sca
     _fit(ctx, "ctx", (B,), torch.int32, dev)
     _fit(tree, "tree", (B, T), torch.int64, dev)
     code = _code(dtype)
-    with _on(dev, stream):
-        if o is None:
-            o = torch.empty_like(q)
-        else:
-            _fit(o, "o", q.shape, dtype, dev)
-        if workspace is None:
-            need = _lib.sala_tree_decode_paged_workspace(B, H, Hkv, T, max_ctx, d)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        else:
-            _fit(workspace, "workspace", workspace.shape, torch.uint8, dev)
-        r = _lib.sala_tree_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
-                                        n_pages, page_table.data_ptr(), page_table.shape[1],
-                                        ctx.data_ptr(), max_ctx, tree.data_ptr(), o.data_ptr(), B, H,
-                                        Hkv, T, d, 64, scale, workspace.data_ptr(), workspace.numel(),
-                                        fmt, code, _raw_stream(dev.index))
-    _check(r, "sala_tree_decode_paged")
+    other = _switch(dev, stream)
+    if other is not None:
+        with other:
+            return tree_decode_paged(q, k_pages, v_pages, page_table, ctx, max_ctx, tree, k_scale, v_scale,
+                                     o, scale, workspace)
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _fit(o, "o", q.shape, dtype, dev)
+    if workspace is None:
+        need = _lib.sala_tree_decode_paged_workspace(B, H, Hkv, T, max_ctx, d)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    else:
+        _lies(workspace, "workspace", torch.uint8, dev)
+    _check(_lib.sala_tree_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
+                                       n_pages, page_table.data_ptr(), page_table.shape[1],
+                                       ctx.data_ptr(), max_ctx, tree.data_ptr(), o.data_ptr(), B, H, Hkv,
+                                       T, d, 64, scale, workspace.data_ptr(), workspace.numel(), fmt, code,
+                                       _raw_stream(dev.index)), "sala_tree_decode_paged")
     return o
 
 
