@@ -995,6 +995,7 @@ sala_status sala_tree_decode_paged(const void* q, const void* k_pages, const voi
         return s;
     REQUIRE(max_ctx >= 0 && (int64_t)max_ctx + T <= (int64_t)max_pages * 64, SALA_ERR_INVALID_ARG,
             "max_ctx %d + T %d outside the page table (%d pages of 64 tokens)", max_ctx, T, max_pages);
+    REQUIRE(max_ctx <= 1 << 30, SALA_ERR_UNSUPPORTED, "max_ctx %d above 2^30", max_ctx);
     REQUIRE((int64_t)B * Hkv <= 65535, SALA_ERR_UNSUPPORTED, "B * Hkv = %lld above 65535",
             (long long)B * Hkv);
     REQUIRE((int64_t)(H / Hkv) * T <= 1 << 20, SALA_ERR_UNSUPPORTED, "more than 2^20 rows per KV head");

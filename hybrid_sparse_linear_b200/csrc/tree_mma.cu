@@ -395,6 +395,18 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     __syncwarp();
                 }
             }
+            if constexpr (F == KvFormat::E4M3 && tail) {
+                // Slots behind the last token may hold anything, e4m3's NaN code too, which zero weights would
+                // not hide: they become zero, and so does that code in a draft's row (no write makes it).
+                for (int e = lane; e < kPage * kPieces; e += 32) {
+                    const int r = e / kPieces, dr = k0 + r - c.ctx;
+                    if (dr < 0) continue;
+                    uint4* u = reinterpret_cast<uint4*>(piece<L>(V, r, e % kPieces));
+                    auto clean = [&](uint32_t w) { return dr >= s.T ? 0u : w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); };
+                    *u = make_uint4(clean(u->x), clean(u->y), clean(u->z), clean(u->w));
+                }
+                __syncwarp();
+            }
 #pragma unroll
             for (int jj = 0; jj < 4; ++jj) {
                 uint32_t pa[4];
@@ -440,7 +452,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     }
                 }
             }
-            if (!kCodes && tail) fence_proxy_async_smem();  // the next copy comes behind the zeros
+            if (F != KvFormat::Int8 && tail) fence_proxy_async_smem();  // the next copy comes behind the zeros
             return true;
             };
             if (!(k0 + kPage > c.ctx ? rest(std::true_type{}) : rest(std::false_type{}))) break;

@@ -602,7 +602,7 @@ def packed_prefill(q, k, v, cu_seqlens, o=None, scale=0.0, stream=None):
     else:
         _fit(o, "o", q.shape, dtype, dev)
     _check(_lib.sala_packed_prefill(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
-                                    o.data_ptr(), B, H, k.shape[0], total, d, scale, code,
+                                    o.data_ptr(), B, H, k.shape[0], total, d, float(scale), code,
                                     _raw_stream(dev.index)), "sala_packed_prefill")
     return o
 
@@ -644,6 +644,7 @@ def kv_read(k_pages, v_pages, page_table, cu_seqlens, pos, total, dtype, k_scale
     B = _offsets_batch(cu_seqlens, dev)
     _fit(pos, "pos", (B,), torch.int32, dev)
     n_pages, Hkv, d, fmt, ks, vs = _pool(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype, dev)
+    total = int(total)
     if not 0 <= total < 1 << 31:
         raise ValueError(f"total {total} outside [0, 2^31)")
     code = _code(dtype)
@@ -677,7 +678,8 @@ def tree_decode_paged(q, k_pages, v_pages, page_table, ctx, max_ctx, tree, k_sca
     """Attention of T new tokens per sequence (T = 1: a decode step; T <= 64: a tree of drafts) over
     the paged cache, which holds ctx[b] tokens of context and the T new ones behind them.
     q: [B, H, T, d]; ctx [B] int32, each <= max_ctx; tree [B, T] int64, bit j of row t set when new
-    token t attends to new token j.  Pages and scales as in kv_write.  Returns o [B, H, T, d]."""
+    token t attends to new token j.  Pages and scales as in kv_write.  Returns o [B, H, T, d].
+    Forward only."""
     _need(q, "q")
     if q.dim() != 4:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected (B, H, T, d)")
@@ -685,6 +687,7 @@ def tree_decode_paged(q, k_pages, v_pages, page_table, ctx, max_ctx, tree, k_sca
     n_pages, Hkv, dp, fmt, ks, vs = _pool(k_pages, v_pages, page_table, k_scale, v_scale, B, dtype, dev)
     if dp != d:
         raise ValueError(f"q has head dim {d}, the pages {dp}")
+    max_ctx = int(max_ctx)
     if not 0 <= max_ctx < 1 << 31:
         raise ValueError(f"max_ctx {max_ctx} outside [0, 2^31)")
     _fit(ctx, "ctx", (B,), torch.int32, dev)
@@ -707,7 +710,8 @@ def tree_decode_paged(q, k_pages, v_pages, page_table, ctx, max_ctx, tree, k_sca
     _check(_lib.sala_tree_decode_paged(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ks, vs,
                                        n_pages, page_table.data_ptr(), page_table.shape[1],
                                        ctx.data_ptr(), max_ctx, tree.data_ptr(), o.data_ptr(), B, H, Hkv,
-                                       T, d, 64, scale, workspace.data_ptr(), workspace.numel(), fmt, code,
+                                       T, d, 64, float(scale), workspace.data_ptr(),
+                                       workspace.numel(), fmt, code,
                                        _raw_stream(dev.index)), "sala_tree_decode_paged")
     return o
 

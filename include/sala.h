@@ -518,7 +518,8 @@ sala_status sala_packed_prefill(const void* q, const void* k, const void* v,
  *   SALA_KV_E4M3 : scale = the smallest power of two with a / scale <= 448, code = e4m3(x / scale),
  *                  round to nearest even (both x / scale and code * scale are exact)
  * A row that holds an infinity or a NaN gets the scale NaN and codes 0, so that every use of it
- * gives NaN.  SALA_KV_SAME copies the rows.
+ * gives NaN; e4m3's own NaN code is never written, and what a caller's own NaN code stands for is
+ * not defined.  SALA_KV_SAME copies the rows.
  * k, v       : [Hkv, total, d] device, dt.   pos : [B] int32 device, >= 0.
  * block      : 64 (tokens per page).   d : 64 or 128.
  * Two rows written to one slot by one call leave either of them, or a mix: give each token once. */
@@ -545,7 +546,7 @@ sala_status sala_kv_read(const void* k_pages, const void* v_pages, const float* 
  * drafts those are the bits of its ancestors and its own.  A row that attends to nothing gives 0.
  * q, o       : [B, H, T, d] device, dt.   1 <= T <= 64.
  * ctx        : [B] int32 device, each in [0, max_ctx] (outside: flagged and clamped).
- * max_ctx    : the largest context, max_ctx + T <= max_pages * 64.
+ * max_ctx    : the largest context, max_ctx + T <= max_pages * 64, at most 2^30.
  * tree       : [B, T] uint64 device; bits at and above T are ignored.
  * scale      : 0 selects 1/sqrt(d); finite and >= 0.   d : 64 or 128.   block : 64.
  * workspace  : at least sala_tree_decode_paged_workspace(...) bytes of device scratch, 16-byte

@@ -302,6 +302,50 @@ def test_tree_decode(sala, H, Hkv, d, dtype, fmt, T, ctx):
     _close(out.t, *_tree_ref(q, cache, ctx, tree), max(ctx) + T, _tag(dtype, "tree"))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("fmt", ["same", "int8", "e4m3"])
+@pytest.mark.parametrize("T,ctx", [(1, [0, 65, 130, 63]), (8, [1, 100, 128]), (64, [70])])
+def test_tree_decode_any_bytes_in_unused_slots(sala, dtype, fmt, T, ctx):
+    # slots behind the last token and pages no one owns hold every byte, and scales of every kind
+    q, cache, tree = _tree_inputs(32, 2, 128, dtype, fmt, T, ctx, seed=6)
+    used = torch.zeros((cache.n_pages, 64), dtype=torch.bool)
+    for b, c in enumerate(ctx):
+        p = torch.arange(c + T)
+        used[cache.table[b][p // 64].long(), p % 64] = True
+    free = ~used[:, None, :].expand(-1, 2, -1)
+    g = _gen(7)
+    for x in (cache.k, cache.v):
+        raw = x.view(torch.uint8)
+        noise = torch.randint(0, 256, raw.shape, generator=g, dtype=torch.uint8)
+        noise[..., ::7] = 0x7f  # e4m3's NaN; in the wider types' upper bytes NaN and infinities
+        noise[..., 1::7] = 0xff
+        raw[free] = noise[free]
+    if cache.ks is not None:
+        odd = torch.tensor([NAN, math.inf, -math.inf, -1.0, 0.0, 1e30, 1e-40])
+        for x in (cache.ks, cache.vs):
+            x[free] = odd[torch.randint(0, 7, x.shape, generator=g)][free]
+    out = _tree_run(sala, q, cache, ctx, tree)
+    sala.check_status()
+    _close(out, *_tree_ref(q, cache, ctx, tree), max(ctx) + T, _tag(dtype, "any bytes"))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("T", [1, 8])
+def test_tree_decode_scales_far_apart(sala, fmt, T):
+    # V rows whose scales differ by 2^80, one row of zeros, and queries far from 1
+    ctx = [300, 40]
+    q, cache, tree = _tree_inputs(32, 2, 128, BF16, fmt, T, ctx, seed=8)
+    q[0] *= 2.0 ** 40
+    q[1, :, ::3] *= 2.0 ** -30
+    cache.ks[cache.table[0, :5].long()] *= 2.0 ** -40   # the logits stay as they were
+    e = torch.randint(-40, 41, cache.vs.shape, generator=_gen(9)).float()
+    cache.vs.mul_(torch.exp2(e))
+    cache.vs[int(cache.table[0, 0]), :, 5] = 0.0
+    out = _tree_run(sala, q, cache, ctx, tree)
+    sala.check_status()
+    _close(out, *_tree_ref(q, cache, ctx, tree), 310, _tag(BF16, "far scales"))
+
+
 @pytest.mark.parametrize("dtype,fmt", [(BF16, "same"), (BF16, "int8"), (F32, "e4m3")])
 def test_tree_decode_peaked_rows_and_a_scale(sala, dtype, fmt):
     q, cache, tree = _tree_inputs(32, 2, 128, dtype, fmt, 4, [600, 90], seed=1, mul=3.0)
