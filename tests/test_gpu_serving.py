@@ -263,6 +263,16 @@ TREE = [
     (32, 2, 128, F32, "same", 1, [500, 0]),
     (8, 2, 64, F32, "int8", 9, [100, 64]),
     (6, 2, 128, F32, "e4m3", 64, [70]),
+    # contexts long enough to be split over CTAs, and CTAs with several items
+    (32, 2, 128, BF16, "same", 1, [5000, 0, 1700, 64, 2999]),
+    (32, 2, 128, BF16, "int8", 1, [4000, 1, 2111]),
+    (32, 2, 128, BF16, "e4m3", 1, [63, 7000]),
+    (8, 2, 64, BF16, "int8", 4, [6000, 0, 33]),
+    (16, 1, 128, BF16, "e4m3", 8, [5000, 700, 0, 0, 129]),
+    (32, 2, 128, BF16, "same", 5, [3000, 64, 1000, 2, 0, 511]),
+    (32, 2, 128, BF16, "int8", 40, [1500, 0, 300]),
+    (8, 2, 64, BF16, "same", 64, [2500]),
+    (32, 2, 128, F32, "int8", 2, [2000, 0, 100]),
 ]
 
 
@@ -442,6 +452,35 @@ def test_tree_decode_bad_pages_and_contexts_are_flagged(sala, dtype, fmt):
         with pytest.raises(sala.SalaError) as err:
             sala.check_status()
         assert err.value.code == sala.ERR_BOUNDS
+
+
+def test_tree_decode_pages_shared_by_sequences(sala):
+    # two sequences with a common prefix of 128 tokens in the same pages
+    q, cache, tree = _tree_inputs(32, 2, 128, BF16, "int8", 2, [200, 180], seed=13)
+    cache.table[1, :2] = cache.table[0, :2]
+    out = _tree_run(sala, q, cache, [200, 180], tree)
+    sala.check_status()
+    _close(out, *_tree_ref(q, cache, [200, 180], tree), 202, "bf16 shared pages")
+
+
+def test_more_sequences_than_the_staged_offsets(sala):
+    # 1500 short sequences: the cache calls search the offsets in global memory
+    g = _gen(14)
+    lens = [int(x) for x in torch.randint(0, 4, (1500,), generator=g)]
+    n, Hkv, d = sum(lens), 2, 128
+    q, k, v = _packed_inputs(32, Hkv, d, BF16, n, seed=15)
+    cu, pos = sp.offsets(lens).cuda(), torch.randint(0, 60, (1500,), generator=g, dtype=torch.int32).cuda()
+    o = sala.packed_prefill(q.cuda(), k.cuda(), v.cuda(), cu)
+    table = torch.randperm(1500, generator=g).to(torch.int32)[:, None].contiguous().cuda()
+    kp, vp = (torch.zeros((1500, Hkv, 64, d), dtype=BF16, device="cuda") for _ in range(2))
+    sala.kv_write(k.cuda(), v.cuda(), cu, pos, table, kp, vp)
+    rk, rv = sala.kv_read(kp, vp, table, cu, pos, n, BF16)
+    sala.check_status()
+    assert torch.equal(rk.cpu(), k) and torch.equal(rv.cpu(), v)
+    b = torch.searchsorted(cu.cpu().long(), torch.arange(n), right=True) - 1
+    at = pos.cpu().long()[b] + torch.arange(n) - cu.cpu().long()[b]
+    assert torch.equal(kp.cpu()[table.cpu()[b, 0].long(), :, at].transpose(0, 1), k)
+    _close(o, *sp.packed64(q, k, v, lens), 4, "bf16 short sequences")
 
 
 # ---------------------------------------------------------------------------------------------
