@@ -282,38 +282,28 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
             __syncwarp();
             load(next, true);
-            // Softmax and P V, once for pages that every row sees whole and once for the others.
-            auto rest = [&](auto masked) -> bool {
-            constexpr bool tail = decltype(masked)::value;
-            uint32_t seen[2] = {0xffffffffu, 0xffffffffu};  // per row: bit 2 j + i of this lane's columns
-            if constexpr (tail) {
+            // A page with drafts or with slots behind the last token: what a row does not see becomes -inf, whose
+            // weight is zero, so that one code serves every page.
+            const bool tail = k0 + kPage > c.ctx;
+            if (tail) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    seen[h] = 0u;
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const int dr = k0 + 8 * j + key_of<L>(2 * t + x) - c.ctx;  // draft number
-                            if (dr < 0 || (dr < 64 && ((bits[h] >> dr) & 1ull))) seen[h] |= 1u << (2 * j + x);
+                            if (dr >= 0 && (dr >= 64 || !((bits[h] >> dr) & 1ull))) sc[j][2 * h + x] = -INFINITY;
                         }
-                }
             }
-            [[maybe_unused]] float alpha[2], nb[2], nv_[2] = {0.f, 0.f};  // nb, nv_: added to the exponents of l's and of O's weights
+            // nb, nv_: added to the exponents of l's and of O's weights; alpha: O's factor
+            [[maybe_unused]] float alpha[2], nb[2], nv_[2] = {0.f, 0.f};
             if constexpr (!kCodes) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if constexpr (!tail) {
-                            mx = max3n(mx, sc[j][2 * h], sc[j][2 * h + 1]);
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                if ((seen[h] >> (2 * j + x)) & 1u) mx = max2n(mx, sc[j][2 * h + x]);
-                        }
-                    }
+                    for (int j = 0; j < 8; ++j) mx = max3n(mx, sc[j][2 * h], sc[j][2 * h + 1]);
                     mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = max2n(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     alpha[h] = st[h].raise(mx * sl2);
@@ -322,11 +312,28 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             }
             if (!__all_sync(0xffffffffu, wait_long(vbar, (nv - 1) & 1, ctx))) {
                 dead = true;
-                return false;
+                break;
             }
             if constexpr (kCodes) {
-                vlg[lane] = lg2(vsc[lane]);
-                vlg[lane + 32] = lg2(vsc[lane + 32]);
+                if (!tail) {
+                    vlg[lane] = lg2(vsc[lane]);
+                    vlg[lane + 32] = lg2(vsc[lane + 32]);
+                } else {
+                    // A scale that is no number must reach the rows that see its draft and no other.
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int r = lane + 32 * x, dr = k0 + r - c.ctx;
+                        const float v = lg2(vsc[r]);
+                        const bool odd = dr >= 0 && !(fabsf(v) < INFINITY) && vsc[r] != 0.f;
+                        vlg[r] = odd ? 0.f : v;
+                        const unsigned who = __ballot_sync(0xffffffffu, odd && dr < s.T);
+                        const int d0 = k0 + 32 * x - c.ctx;  // draft number of lane 0's row
+                        const uint64_t drafts = d0 >= 0 ? (d0 < 64 ? (uint64_t)who << d0 : 0ull) : who >> min(-d0, 31);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (bits[h] & drafts) st[h].l = __uint_as_float(0x7fffffffu);
+                    }
+                }
                 __syncwarp();
                 float mx[2] = {-INFINITY, -INFINITY}, mv[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -335,14 +342,8 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float y0 = sc[j][2 * h] *= sl[h], y1 = sc[j][2 * h + 1] *= sl[h];
-                        if (!tail || ((seen[h] >> (2 * j)) & 1u)) {
-                            mx[h] = max2n(mx[h], y0);
-                            mv[h] = max2n(mv[h], y0 + va);
-                        }
-                        if (!tail || ((seen[h] >> (2 * j + 1)) & 1u)) {
-                            mx[h] = max2n(mx[h], y1);
-                            mv[h] = max2n(mv[h], y1 + vb);
-                        }
+                        mx[h] = max3n(mx[h], y0, y1);
+                        mv[h] = max3n(mv[h], y0 + va, y1 + vb);
                     }
                 }
 #pragma unroll
@@ -354,7 +355,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     }
                     (void)st[h].raise(mx[h]);
                     nb[h] = st[h].shift();
-                    alpha[h] = 1.f;  // of O
+                    alpha[h] = 1.f;
                     if (mv[h] > top_v[h] + kGrow) {
                         if (top_v[h] != -INFINITY) alpha[h] = ex2(top_v[h] - mv[h]);
                         top_v[h] = mv[h];
@@ -373,9 +374,10 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
             }
             if constexpr (!kCodes) {
-                if constexpr (tail) {  // V's rows that not every row sees: see tree_tc.cu
+                if (tail) {  // V's rows that not every row sees: see tree_tc.cu
                     constexpr int kC = D / 8;
-                    for (int e = lane; e < kPage * kC; e += 32) {
+#pragma unroll 4
+                    for (int e = max(c.ctx - k0, 0) * kC + lane; e < kPage * kC; e += 32) {
                         const int r = e / kC, p = e % kC, dr = k0 + r - c.ctx;
                         uint4* u = reinterpret_cast<uint4*>(piece<L>(V, r, p));
                         if (dr >= s.T) {
@@ -395,12 +397,12 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     __syncwarp();
                 }
             }
-            if constexpr (F == KvFormat::E4M3 && tail) {
+            if (F == KvFormat::E4M3 && tail) {
                 // Slots behind the last token may hold anything, e4m3's NaN code too, which zero weights would
                 // not hide: they become zero, and so does that code in a draft's row (no write makes it).
-                for (int e = lane; e < kPage * kPieces; e += 32) {
+#pragma unroll 4
+                for (int e = max(c.ctx - k0, 0) * kPieces + lane; e < kPage * kPieces; e += 32) {
                     const int r = e / kPieces, dr = k0 + r - c.ctx;
-                    if (dr < 0) continue;
                     uint4* u = reinterpret_cast<uint4*>(piece<L>(V, r, e % kPieces));
                     auto clean = [&](uint32_t w) { return dr >= s.T ? 0u : w & ~__vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); };
                     *u = make_uint4(clean(u->x), clean(u->y), clean(u->z), clean(u->w));
@@ -420,16 +422,15 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const bool s0 = !tail || ((seen[h] >> (2 * j)) & 1u), s1 = !tail || ((seen[h] >> (2 * j + 1)) & 1u);
                         const float x0 = sc[j][2 * h], x1 = sc[j][2 * h + 1];
                         if constexpr (kCodes) {
-                            st[h].l += (s0 ? ex2(x0 + nb[h]) : 0.f) + (s1 ? ex2(x1 + nb[h]) : 0.f);
-                            const __half2 w = __floats2half2_rn(s0 ? ex2(x0 + (va + nv_[h])) : 0.f, s1 ? ex2(x1 + (vb + nv_[h])) : 0.f);
+                            st[h].l += ex2(x0 + nb[h]) + ex2(x1 + nb[h]);
+                            const __half2 w = __floats2half2_rn(ex2(x0 + (va + nv_[h])), ex2(x1 + (vb + nv_[h])));
                             pa[2 * y + h] = *reinterpret_cast<const uint32_t*>(&w);
                         } else {
                             const float p0 = ex2(fmaf(x0, sl2, nb[h])), p1 = ex2(fmaf(x1, sl2, nb[h]));
-                            st[h].l += (s0 ? p0 : 0.f) + (s1 ? p1 : 0.f);
-                            pa[2 * y + h] = pack_bf16x2(s0 ? p0 : 0.f, s1 ? p1 : 0.f);
+                            st[h].l += p0 + p1;
+                            pa[2 * y + h] = pack_bf16x2(p0, p1);
                         }
                     }
                 }
@@ -453,9 +454,6 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
             }
             if (F != KvFormat::Int8 && tail) fence_proxy_async_smem();  // the next copy comes behind the zeros
-            return true;
-            };
-            if (!(k0 + kPage > c.ctx ? rest(std::true_type{}) : rest(std::false_type{}))) break;
             __syncwarp();
             id = next;
             load(id, false);
