@@ -6,7 +6,7 @@
 // with 4 x D/16 sums per thread.  Per tile 2 * 64 * 64 * D multiply-adds against 2 * 64 * D loads: the
 // fp32 FMA units are the bound once the loads are out of the way, so V's tile is on its way into
 // registers while S is formed and the next K's while P V is (loads at the point of use: 150 us for the
-// 2049 ragged tokens of eight heads of 64 that take XX us).
+// 2049 ragged tokens of eight heads of 64 that take 139 us).
 //
 // Masked positions are left out by selection, never by adding a large negative number or by
 // multiplying with zero: a hidden key or value may hold an infinity or a NaN without touching the

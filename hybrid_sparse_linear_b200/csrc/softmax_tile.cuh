@@ -1,5 +1,5 @@
-// The softmax side of dense attention on the tensor cores: a thread owns one row of a 128 x 128
-// tile of logits S in tensor memory (TMEM lane = row) and turns it into bf16 probabilities over
+// The softmax side of dense attention on the tensor cores: a thread owns one row of a tile of
+// logits S (128 rows, 64 keys) in tensor memory (TMEM lane = row) and turns it into bf16 probabilities over
 // S's own columns, keeping the row's running maximum and sum in registers.
 //
 // The maximum is kept stale until a row's new one exceeds it by more than 8 in log2 units: a
@@ -19,7 +19,6 @@ namespace smx {
 
 using namespace ptx;
 
-constexpr int kKeys = 128;      // columns of a tile
 constexpr float kGrow = 8.f;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -87,10 +86,6 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, const 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const DevCtx& ctx,
                                           volatile int* abort) {
     return __all_sync(0xffffffffu, wait_or_abort(bar, parity, ctx, abort));
-}
-
-__device__ __forceinline__ uint32_t (&chunk(uint32_t (&a)[kKeys], int c))[32] {
-    return *reinterpret_cast<uint32_t(*)[32]>(a + 32 * c);
 }
 
 // Maximum of 32 logits; of those whose bit in seen is set (-inf when none is).

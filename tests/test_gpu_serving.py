@@ -420,6 +420,17 @@ def test_tree_decode_batch_longer_than_a_warp_and_same_bits(sala):
     _close(a, *_tree_ref(q, cache, ctx, tree), 410, "bf16 batch")
 
 
+@pytest.mark.parametrize("fmt,n,top", [("int8", 64, 2500), ("same", 64, 2500), ("same", 10, 2500), ("int8", 64, 4200)])
+def test_tree_decode_many_items_of_middle_lengths(sala, fmt, n, top):
+    # a block per item, or equal runs of pages over the blocks, by the number of items and their pages
+    g = _gen(12)
+    ctx = [top, 0, 1, 64] + [int(x) for x in torch.randint(0, 300, (n - 4,), generator=g)]
+    q, cache, tree = _tree_inputs(32, 2, 128, BF16, fmt, 1, ctx, seed=11, fill=NAN)
+    out = _tree_run(sala, q, cache, ctx, tree)
+    sala.check_status()
+    _close(out, *_tree_ref(q, cache, ctx, tree), top + 1, "bf16 many items")
+
+
 @pytest.mark.parametrize("dtype,fmt", [(BF16, "same"), (BF16, "e4m3"), (F32, "same")])
 def test_tree_decode_bad_pages_and_contexts_are_flagged(sala, dtype, fmt):
     ctx = [200, 100]
