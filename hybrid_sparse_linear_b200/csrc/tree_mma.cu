@@ -17,10 +17,12 @@
 //
 // Codes are multiplied as fp16, which they are exactly and which takes two to three instructions a
 // pair where bf16 takes five (the conversion is half of the kernel's instructions).  Q's rows are
-// brought to it by a power of two that puts their largest value in [1, 2); what falls below fp16's
-// smallest step then is 2^-25 of that value.  P has no such bound, as it carries the scales of V's
-// rows: the weight of key j in O is 2^(y_j + log2 sv_j - M) with a running maximum M of its own
-// exponent, the one in the row's sum 2^(y_j - m) as ever, and O is brought to m at the item's end.
+// brought to it by a power of two that puts their largest value in [2^14, 2^15); what falls below fp16's
+// smallest step then is 2^-39 of that value.  P has no such bound, as it carries the scales of V's
+// rows: the weight of key j in O is 2^(y_j + log2 sv_j - M + 7) with a running maximum M of its own
+// exponent, which is stale by at most 8, so that weights stay below 2^15 and vanish 2^-32 under the
+// largest of the warp's keys (a million of those lose 2^-12 of it); the weight in the row's sum is
+// 2^(y_j - m) as ever, and O is brought to m at the item's end.
 //
 // Hidden positions, infinities and NaN: as in the tensor-core kernel (tree_tc.cu).  The warps'
 // accumulators are joined in shared memory at an item's end.
@@ -40,6 +42,8 @@ using namespace smx;
 using namespace dec;
 
 constexpr int kRows = 16;
+constexpr int kUpQ = 14;      // Q's largest value, and 2^kUpP the weight of a key at M, in fp16
+constexpr float kUpP = 7.f;
 
 template <int D, KvFormat F>
 struct Layout {
@@ -173,47 +177,47 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         float sl[2] = {sl2, sl2};  // per row: from S to log2 units
         uint4* qf = reinterpret_cast<uint4*>(sm + L::kOffQ) + lane;
         {
-        uint32_t qa[kSteps][4];
+            uint32_t qa[kSteps][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = g + 8 * h;
-            const bool real = r < s.rows;
-            bits[h] = real ? tree::draft_bits(masks, c.b, r % s.T, s.T) : 0ull;
-            const __nv_bfloat16* src = q + (row0 + r) * D + t * kPer;
-#pragma unroll
-            for (int st = 0; st < kSteps; ++st) {
-                const uint2 u = real ? __ldg(reinterpret_cast<const uint2*>(
-                                           src + (st / (kPer / 4)) * 4 * kPer + (st % (kPer / 4)) * 4))
-                                     : make_uint2(0u, 0u);
-                qa[st][h] = u.x;
-                qa[st][2 + h] = u.y;
-            }
-            if constexpr (kCodes) {  // to fp16, the largest value in [1, 2)
-                uint32_t m = 0u;
-#pragma unroll
-                for (int st = 0; st < kSteps; ++st)
-                    m = __vmaxu2(m, __vmaxu2(qa[st][h] & 0x7fff7fffu, qa[st][2 + h] & 0x7fff7fffu));
-                m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                int ex = (int)(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent
-                if (ex == 255) ex = 127;                         // an infinity or a NaN stays what it is
-                ex = min(max(ex, 1), 253);
-                const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-                sl[h] = sl2 * __uint_as_float((uint32_t)ex << 23);
-                auto half2 = [&](uint32_t w) {
-                    const __half2 v = __floats2half2_rn(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
-                    return *reinterpret_cast<const uint32_t*>(&v);
-                };
+            for (int h = 0; h < 2; ++h) {
+                const int r = g + 8 * h;
+                const bool real = r < s.rows;
+                bits[h] = real ? tree::draft_bits(masks, c.b, r % s.T, s.T) : 0ull;
+                const __nv_bfloat16* src = q + (row0 + r) * D + t * kPer;
 #pragma unroll
                 for (int st = 0; st < kSteps; ++st) {
-                    qa[st][h] = half2(qa[st][h]);
-                    qa[st][2 + h] = half2(qa[st][2 + h]);
+                    const uint2 u = real ? __ldg(reinterpret_cast<const uint2*>(
+                                               src + (st / (kPer / 4)) * 4 * kPer + (st % (kPer / 4)) * 4))
+                                         : make_uint2(0u, 0u);
+                    qa[st][h] = u.x;
+                    qa[st][2 + h] = u.y;
+                }
+                if constexpr (kCodes) {  // to fp16, the largest value in [2^kUpQ, 2^(kUpQ + 1))
+                    uint32_t m = 0u;
+#pragma unroll
+                    for (int st = 0; st < kSteps; ++st)
+                        m = __vmaxu2(m, __vmaxu2(qa[st][h] & 0x7fff7fffu, qa[st][2 + h] & 0x7fff7fffu));
+                    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                    int ex = (int)(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent
+                    if (ex == 255) ex = 127;                         // an infinity or a NaN stays what it is
+                    ex = max(ex, kUpQ + 1) - kUpQ;
+                    const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+                    sl[h] = sl2 * __uint_as_float((uint32_t)ex << 23);
+                    auto half2 = [&](uint32_t w) {
+                        const __half2 v = __floats2half2_rn(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
+                        return *reinterpret_cast<const uint32_t*>(&v);
+                    };
+#pragma unroll
+                    for (int st = 0; st < kSteps; ++st) {
+                        qa[st][h] = half2(qa[st][h]);
+                        qa[st][2 + h] = half2(qa[st][2 + h]);
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st)  // every warp has them all; one puts them down
-            if (st % L::kWarps == warp) qf[st * 32] = make_uint4(qa[st][0], qa[st][1], qa[st][2], qa[st][3]);
+            for (int st = 0; st < kSteps; ++st)  // every warp has them all; one puts them down
+                if (st % L::kWarps == warp) qf[st * 32] = make_uint4(qa[st][0], qa[st][1], qa[st][2], qa[st][3]);
         }
         if constexpr (!kCodes) {
             if (tid == 0) noted = 0;
@@ -361,7 +365,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         top_v[h] = mv[h];
                     }
                     if (!(mv[h] <= 3.402823466e38f)) st[h].l = __uint_as_float(0x7fffffffu);
-                    nv_[h] = top_v[h] == -INFINITY ? 0.f : -top_v[h];
+                    nv_[h] = top_v[h] == -INFINITY ? 0.f : kUpP - top_v[h];
                 }
             }
             if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
@@ -468,7 +472,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             if (t == 0) ml[warp * kRows + g + 8 * h] = make_float2(st[h].m, l);
             float* dst = reinterpret_cast<float*>(K) + (g + 8 * h) * D;
             if constexpr (kCodes) {  // O from M to m
-                const float f = top_v[h] == -INFINITY ? 0.f : ex2(top_v[h] - (st[h].m == -INFINITY ? 0.f : st[h].m));
+                const float f = top_v[h] == -INFINITY ? 0.f : ex2(top_v[h] - kUpP - (st[h].m == -INFINITY ? 0.f : st[h].m));
 #pragma unroll
                 for (int e = 0; e < D / 8; ++e) {
                     o[e][2 * h] *= f;

@@ -518,8 +518,8 @@ sala_status sala_packed_prefill(const void* q, const void* k, const void* v,
  *   SALA_KV_E4M3 : scale = the smallest power of two with a / scale <= 448, code = e4m3(x / scale),
  *                  round to nearest even (both x / scale and code * scale are exact)
  * A row that holds an infinity or a NaN gets the scale NaN and codes 0, so that every use of it
- * gives NaN; e4m3's own NaN code is never written, and what a caller's own NaN code stands for is
- * not defined.  SALA_KV_SAME copies the rows.
+ * gives NaN; e4m3's own NaN code is never written, and what a caller's own NaN code or negative scale
+ * stands for is not defined.  SALA_KV_SAME copies the rows.
  * k, v       : [Hkv, total, d] device, dt.   pos : [B] int32 device, >= 0.
  * block      : 64 (tokens per page).   d : 64 or 128.
  * Two rows written to one slot by one call leave either of them, or a mix: give each token once. */
@@ -543,7 +543,8 @@ sala_status sala_kv_read(const void* k_pages, const void* v_pages, const float* 
  * drafted tokens, and with T = 1 the plain decode step.  Sequence b's cache holds ctx[b] tokens of
  * context and behind them the T new ones (written there by sala_kv_write).  Row t attends to the
  * whole context and to the new token j exactly when bit j of tree[b][t] is set; for a tree of
- * drafts those are the bits of its ancestors and its own.  A row that attends to nothing gives 0.
+ * drafts those are the bits of its ancestors and its own.  A row that attends to nothing, or whose
+ * logits are all -infinity, gives 0.
  * q, o       : [B, H, T, d] device, dt.   1 <= T <= 64.
  * ctx        : [B] int32 device, each in [0, max_ctx] (outside: flagged and clamped).
  * max_ctx    : the largest context, max_ctx + T <= max_pages * 64, at most 2^30.

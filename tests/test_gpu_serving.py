@@ -356,6 +356,35 @@ def test_tree_decode_scales_far_apart(sala, fmt, T):
     _close(out, *_tree_ref(q, cache, ctx, tree), 310, _tag(BF16, "far scales"))
 
 
+@pytest.mark.parametrize("dtype,fmt,T", [(BF16, "int8", 1), (BF16, "e4m3", 1), (BF16, "same", 1), (BF16, "int8", 16),
+                                         (F32, "int8", 1)])
+def test_tree_decode_one_key_above_a_long_flat_tail(sala, dtype, fmt, T):
+    # One key of 700032 weighs 1, each other 2^-25.5, which together is 1.5 % of it: nearly twice the bound.
+    # Every tail page of the table is the same page; the result follows from the two kinds of keys.
+    n, d, w = 700032, 64, 2.0 ** -25.5
+    kind = {"same": dtype, "int8": torch.int8, "e4m3": torch.float8_e4m3fn}[fmt]
+    k, v = torch.zeros((2, 1, 64, d)), torch.full((2, 1, 64, d), 64.0)
+    k[0, 0, 0, 0] = 64.0
+    v[0, 0, 0] = -64.0
+    v[0, 0, 0, ::2] = 0.0
+    ks, vs = (None, None) if fmt == "same" else (torch.full((2, 1, 64), x).cuda() for x in (1.0, 1.0))
+    q = torch.zeros((1, 1, T, d), dtype=dtype)
+    q[..., 0] = 1.0
+    table = torch.ones((1, n // 64), dtype=torch.int32)
+    table[0, 0] = 0
+    tree = torch.tensor([sp.signed([1 << t for t in range(T)])])  # a row sees the context and itself
+    out = sala.tree_decode_paged(q.cuda(), k.to(kind).cuda(), v.to(kind).cuda(), table.cuda(),
+                                 torch.tensor([n - T], dtype=torch.int32).cuda(), n - T, tree.cuda(), ks, vs,
+                                 scale=25.5 * math.log(2.0) / 64)
+    sala.check_status()
+    tail = (n - T) * w  # the context's keys but one, and the row's own
+    peak = v[0, 0, 0].double()
+    o, A = ((x + tail * 64.0) / (1.0 + tail) for x in (peak, peak.abs()))
+    # the scale is rounded to 32 bits: 2^-24 of a logit of 17.7 on top of the product's error
+    e = torch.full((1, 1, T), 17.7 * (d + 5) * 2.0 ** -24, dtype=torch.float64)
+    _close(out, o.expand(1, 1, T, d), A.expand(1, 1, T, d), e, n, _tag(dtype, "flat tail"))
+
+
 @pytest.mark.parametrize("dtype,fmt", [(BF16, "same"), (BF16, "int8"), (F32, "e4m3")])
 def test_tree_decode_peaked_rows_and_a_scale(sala, dtype, fmt):
     q, cache, tree = _tree_inputs(32, 2, 128, dtype, fmt, 4, [600, 90], seed=1, mul=3.0)
