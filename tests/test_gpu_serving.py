@@ -449,6 +449,28 @@ def test_tree_decode_batch_longer_than_a_warp_and_same_bits(sala):
     _close(a, *_tree_ref(q, cache, ctx, tree), 410, "bf16 batch")
 
 
+@pytest.mark.parametrize("H,Hkv,d,lens", [(8, 2, 64, [70, 1] * 25), (8, 2, 64, [300, 0, 65]), (32, 2, 128, [200, 150]),
+                                          (4, 4, 128, [130, 17])])
+def test_packed_prefill_fp32_block_sizes(sala, H, Hkv, d, lens):
+    # blocks of 32 rows while all of 64 would run at once, else of 64
+    q, k, v = _packed_inputs(H, Hkv, d, F32, sum(lens), seed=21)
+    out = sala.packed_prefill(q.cuda(), k.cuda(), v.cuda(), sp.offsets(lens).cuda())
+    sala.check_status()
+    _close(out, *sp.packed64(q, k, v, lens), max(lens), "fp32 blocks")
+
+
+@pytest.mark.parametrize("fmt", ["same", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d,T,ctx", [(32, 2, 128, 1, [9000]), (32, 2, 128, 2, [700, 0, 64]), (32, 2, 128, 5, [300]),
+                                           (8, 2, 64, 4, [20000, 3]), (8, 2, 64, 7, [1000, 100]), (8, 2, 64, 33, [100]),
+                                           (4, 4, 128, 1, [200] * 9)])
+def test_tree_decode_fp32_block_sizes(sala, H, Hkv, d, T, ctx, fmt):
+    # blocks of 16, 32 and 64 rows; one block per SM, and more
+    q, cache, tree = _tree_inputs(H, Hkv, d, F32, fmt, T, ctx, seed=22, fill=NAN)
+    out = _tree_run(sala, q, cache, ctx, tree)
+    sala.check_status()
+    _close(out, *_tree_ref(q, cache, ctx, tree), max(ctx) + T, "fp32 blocks")
+
+
 @pytest.mark.parametrize("fmt,n,top", [("int8", 64, 2500), ("same", 64, 2500), ("same", 10, 2500), ("int8", 64, 4200)])
 def test_tree_decode_many_items_of_middle_lengths(sala, fmt, n, top):
     # a block per item, or equal runs of pages over the blocks, by the number of items and their pages
