@@ -546,12 +546,12 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 }
 
 // Short contexts: a block per item, with no partials to join.  Few items leave SMs idle, which pays up
-// to about 24 pages (32 items of bf16 pages, one token, in us against equal runs and their join: 16 pages
-// 11 against 14, 24 pages 13.8 against 16.7, 32 pages 16.9 against 18.0, 48 pages 21 against 19; int8
-// 15, 16.4, 20, 25 against 16, 16.7, 18, 22).  Where items nearly fill the SMs it pays up to 64 (128
-// items of 64 pages: bf16 47 against 55, int8 37 against 49; of 1 to 64 pages 32 and 33 against 38 and
-// 35; 200 int8 items of 64 pages lose, 70 against 66), and is even at 128.
-constexpr int kItemPages = 24, kItemPagesFull = 64;
+// to 16 pages (bf16 pages, one token, in us: 2 items of 16 pages 10.9 against 14.1 with equal runs and their
+// join, of 24 pages 13.3 against 12.6), more items up to 24 (32 items of 24 pages 13.9 against 16.7, of 32
+// pages even).  Where items nearly fill the SMs it pays up to 64 (128 items of 64 pages: bf16 47 against 55,
+// int8 37 against 49; of 1 to 64 pages 32 and 33 against 38 and 35; 200 int8 items of 64 pages lose, 70
+// against 66), and is even at 128.
+int item_pages(int items, int sms) { return 4 * items >= 3 * sms ? 64 : 8 * items >= sms ? 24 : 16; }
 // Beginning an item (a round of loads that nothing overlaps, the warps' join) costs about as much as
 // this many pages.
 constexpr int kPad = 12;
@@ -576,9 +576,8 @@ cudaError_t tree_mma(const void* q, const KvPages& pages, const uint64_t* masks,
     if (pages.n_pages > 0 && (!map(&tmK, pages.k) || !map(&tmV, pages.v))) return cudaErrorInvalidValue;
     if (cudaError_t e = ensure_smem<tree_mma_kernel<D, F>>(L::kBytes); e != cudaSuccess) return e;
     const int tiles = (s.max_ctx + s.T + kPage - 1) / kPage, items = s.B * s.Hkv, sms = device_sm_count();
-    const bool by_item = tiles <= (4 * items >= 3 * sms ? kItemPagesFull : kItemPages);
-    const long long most = (long long)items * tiles;
-    const int n_cta = by_item ? items : most < sms ? (int)most : sms;
+    const bool by_item = tiles <= item_pages(items, sms);
+    const int n_cta = by_item ? items : tree::run_ctas(s, tiles, 2, sms);
     const tree::Partials part = tree::partials_at(ws, by_item ? 0 : n_cta, s.rows);
     tree_mma_kernel<D, F><<<n_cta, L::kThreads, L::kBytes, st>>>(
         tmK, tmV, static_cast<const __nv_bfloat16*>(q), pages, masks, static_cast<__nv_bfloat16*>(o), s,

@@ -134,6 +134,16 @@ __device__ __forceinline__ void next_item(const Shape& s, Cursor& c) {
     }
 }
 
+// CTAs of the tensor-core and warp-tile kernels: at most one per SM, and where the tiles are few, `least` to
+// four tiles each, so that an item has up to 32 partials (what the join reads in one pass).  In us, one
+// sequence, 2 KV heads of 16 query heads, bf16: one token over 128 pages 14.9 (a tile per CTA: 24.7), two
+// tokens 18.6 (29.2), over 48 pages 16.7 (18.7).
+inline int run_ctas(const Shape& s, int tiles, int least, int sms) {
+    const int by32 = (tiles + 31) / 32, run = by32 < least ? least : by32 < 4 ? by32 : 4;
+    const long long n = ((long long)s.B * s.Hkv * s.n_rt * tiles + run - 1) / run;
+    return n < sms ? (int)n : sms;
+}
+
 // Bits of the drafts that row t of sequence b attends to.
 __device__ __forceinline__ uint64_t draft_bits(const uint64_t* masks, int b, int t, int T) {
     const uint64_t m = __ldg(reinterpret_cast<const unsigned long long*>(masks) + (int64_t)b * T + t);

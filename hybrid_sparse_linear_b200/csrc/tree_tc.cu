@@ -705,9 +705,7 @@ cudaError_t tree_tc(const void* q, const KvPages& pages, const uint64_t* masks, 
     s.kt = kK;
     s.pad = kPad;
     const int tiles = (s.max_ctx + s.T + kK - 1) / kK;
-    const long long most = (long long)s.B * s.Hkv * s.n_rt * tiles;
-    const int sms = device_sm_count();
-    const int n_cta = most < sms ? (int)most : sms;
+    const int n_cta = tree::run_ctas(s, tiles, 1, device_sm_count());
     const int rt = kWide ? L::kRows : s.rows;
     const tree::Partials part = tree::partials_at(ws, n_cta, rt);
     tree_tc_kernel<D, F, kWide><<<n_cta, L::kThreads, bytes, st>>>(
