@@ -112,15 +112,8 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
     if (by_item) {
         if (tid == 0) {
-            tree::Cursor c;
             bool bad = false;
-            c.b = blockIdx.x / s.Hkv;
-            c.g = blockIdx.x % s.Hkv;
-            c.rt = c.tile = 0;
-            c.ctx = tree::ctx_of(s, c.b, &bad);
-            c.n_tiles = tree::tiles_of(s, c.ctx);
-            c.left = c.n_tiles;
-            cur0 = c;
+            cur0 = tree::item_at(s, blockIdx.x, &bad);
             if (bad) flag(ctx, kStatusBounds);
         }
     } else if (warp == 0) {

@@ -105,6 +105,19 @@ __device__ __forceinline__ Cursor find_place(const Shape& s, long long x, long l
     return c;
 }
 
+// The cursor of a CTA that has item i whole and nothing else (i = (b * Hkv + g) * n_rt + rt).
+__device__ __forceinline__ Cursor item_at(const Shape& s, int i, bool* bad) {
+    Cursor c;
+    c.rt = i % s.n_rt;
+    c.g = i / s.n_rt % s.Hkv;
+    c.b = i / s.n_rt / s.Hkv;
+    c.tile = 0;
+    c.ctx = ctx_of(s, c.b, bad);
+    c.n_tiles = tiles_of(s, c.ctx);
+    c.left = c.n_tiles;
+    return c;
+}
+
 // Places of the cursor's item inside the run, and the tiles among them: [first_tile, first_tile + n).
 __device__ __forceinline__ int run_places(const Cursor& c) {
     const long long n = c.n_tiles - c.tile;

@@ -40,6 +40,16 @@ using namespace smx;
 
 constexpr int kK = 64;              // keys per tile: a page
 constexpr int kConvThreads = 256;
+// Short contexts: a CTA per item, without partials and their join.  Up to 8 tiles it pays for any number of
+// items, up to 16 (wide: 32) where they are three eighths of the SMs, up to 32 (wide: 64) at three quarters.
+// In us, against equal runs, bf16 and 2 KV heads of 16 query heads: two tokens, 8 sequences of 8 pages 13.3
+// against 16.3, of 16 pages 19.0 against 17.7; 32 sequences of 16 pages 19.8 against 22.2, of 32 pages 30
+// against 26; 60 of 32 pages 32 against 41, of 1 to 32 pages 30 and 30, of 64 pages 54 against 60, of 1 to 64
+// pages 53 against 44; 64 drafts (wide), 16 sequences of 2 pages 17 against 41, 8 of 32 pages 48 against
+// 55, of 64 pages 79 against 69, 16 of 64 pages 80 against 118, 50 of 64 pages 236 against 287.
+inline int item_tiles(bool wide, long long items, int sms) {
+    return 8 * items < 3 * sms ? 8 : (4 * items < 3 * sms ? 16 : 32) << (wide ? 1 : 0);
+}
 constexpr int kPad = 4;  // beginning an item (Q, the first tiles' chain, the epilogue) costs about four tiles
 
 template <int D, KvFormat F, bool kWide>
@@ -107,7 +117,8 @@ template <int D, KvFormat F, bool kWide>
 __global__ void __launch_bounds__(Layout<D, F, kWide>::kThreads, 1)
 tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, KvPages pages, const uint64_t* __restrict__ masks,
-               __nv_bfloat16* __restrict__ out, tree::Shape s, tree::Partials part, float sl2, DevCtx ctx) {
+               __nv_bfloat16* __restrict__ out, tree::Shape s, tree::Partials part, bool by_item, float sl2,
+               DevCtx ctx) {
     using L = Layout<D, F, kWide>;
     static_assert(L::kOffBars + sizeof(Bars<L>) <= 227 * 1024, "shared memory");
     constexpr bool kCodes = L::kCodes;
@@ -190,10 +201,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         if (warp == 8) {
             // ------------------------------------------------------------ items and loads
             bool bad = false;
-            const long long w = tree::total_places(s, lane, &bad);
-            if (bad && blockIdx.x == 0) flag(ctx, kStatusBounds);
-            const long long x0 = tree::run_start(w, blockIdx.x, gridDim.x);
-            tree::Cursor c = tree::find_place(s, x0, tree::run_start(w, blockIdx.x + 1, gridDim.x) - x0, lane);
+            tree::Cursor c;
+            if (by_item) {
+                c = tree::item_at(s, blockIdx.x, &bad);
+                if (bad) flag(ctx, kStatusBounds);
+            } else {
+                const long long w = tree::total_places(s, lane, &bad);
+                if (bad && blockIdx.x == 0) flag(ctx, kStatusBounds);
+                const long long x0 = tree::run_start(w, blockIdx.x, gridDim.x);
+                c = tree::find_place(s, x0, tree::run_start(w, blockIdx.x + 1, gridDim.x) - x0, lane);
+            }
             uint32_t rc[2] = {0, 0}, rr = 0, kq = 0, looks = 0;  // entries, raw tiles, Q tiles, looks
             uint32_t via = 0;  // slots whose last load went to v_landed
             bool ok = true;
@@ -705,14 +722,17 @@ cudaError_t tree_tc(const void* q, const KvPages& pages, const uint64_t* masks, 
     s.kt = kK;
     s.pad = kPad;
     const int tiles = (s.max_ctx + s.T + kK - 1) / kK;
-    const int n_cta = tree::run_ctas(s, tiles, 1, device_sm_count());
+    const long long items = (long long)s.B * s.Hkv * s.n_rt;  // below 2^31, as the query rows are
+    const int sms = device_sm_count();
+    const bool by_item = tiles <= item_tiles(kWide, items, sms);
+    const int n_cta = by_item ? (int)items : tree::run_ctas(s, tiles, 1, sms);
     const int rt = kWide ? L::kRows : s.rows;
     const tree::Partials part = tree::partials_at(ws, n_cta, rt);
     tree_tc_kernel<D, F, kWide><<<n_cta, L::kThreads, bytes, st>>>(
         tmQ, tmK, tmV, pages, masks, static_cast<__nv_bfloat16*>(o), s, part,
-        scale * 1.4426950408889634f, ctx);
+        by_item, scale * 1.4426950408889634f, ctx);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    if (tiles == 1) return cudaSuccess;  // no item is ever split
+    if (by_item) return cudaSuccess;
     return launch_tree_join(DType::BF16, part, o, s, rt, D, n_cta, st);
 }
 

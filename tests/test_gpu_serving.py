@@ -482,6 +482,20 @@ def test_tree_decode_many_items_of_middle_lengths(sala, fmt, n, top):
     _close(out, *_tree_ref(q, cache, ctx, tree), top + 1, "bf16 many items")
 
 
+@pytest.mark.parametrize("fmt", ["same", "int8"])
+@pytest.mark.parametrize("T,n,top", [(2, 3, 400), (2, 3, 700), (8, 40, 900), (8, 40, 1200), (2, 60, 1900), (33, 2, 450),
+                                     (33, 2, 600), (64, 16, 2200)])
+def test_tree_decode_items_and_runs(sala, fmt, T, n, top):
+    # a block per item or equal runs of key tiles, on both sides of the choice
+    g = _gen(24)
+    ctx = [top, 0, 64][:n] + [int(x) for x in torch.randint(0, 100, (max(n - 3, 0),), generator=g)]
+    q, cache, tree = _tree_inputs(32, 2, 128, BF16, fmt, T, ctx, seed=23, fill=NAN)
+    a, b = (_tree_run(sala, q, cache, ctx, tree) for _ in range(2))
+    sala.check_status()
+    assert torch.equal(a, b)
+    _close(a, *_tree_ref(q, cache, ctx, tree), top + T, "bf16 items and runs")
+
+
 @pytest.mark.parametrize("dtype,fmt", [(BF16, "same"), (BF16, "e4m3"), (F32, "same")])
 def test_tree_decode_bad_pages_and_contexts_are_flagged(sala, dtype, fmt):
     ctx = [200, 100]
