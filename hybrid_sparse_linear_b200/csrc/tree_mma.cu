@@ -492,17 +492,21 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         for (int e = tid; e < s.rows * (D / 4); e += L::kThreads) {
             const int r = e / (D / 4), col = (e % (D / 4)) * 4;
             float top = -INFINITY;
+            float2 p[L::kWarps];
 #pragma unroll
-            for (int w = 0; w < L::kWarps; ++w) top = fmaxf(top, ml[w * kRows + r].x);
+            for (int w = 0; w < L::kWarps; ++w) {
+                p[w] = ml[w * kRows + r];
+                top = fmaxf(top, p[w].x);
+            }
             float l = 0.f;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < L::kWarps; ++w) {
-                const float2 p = ml[w * kRows + r];
-                if (p.x == -INFINITY && p.y == 0.f) continue;  // saw nothing
-                const float wt = ex2(p.x - top);
-                const float4 y = *reinterpret_cast<const float4*>(sm + w * L::kStage + (r * D + col) * 4);
-                l += wt * p.y;
+                const bool saw = p[w].x != -INFINITY || p[w].y != 0.f;  // else the buffer holds no row
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (saw) y = *reinterpret_cast<const float4*>(sm + w * L::kStage + (r * D + col) * 4);
+                const float wt = saw ? ex2(p[w].x - top) : 0.f;
+                l += wt * p[w].y;
                 x.x += wt * y.x;
                 x.y += wt * y.y;
                 x.z += wt * y.z;

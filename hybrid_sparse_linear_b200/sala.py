@@ -504,6 +504,14 @@ def sparse_decode_paged(q, k_pages, v_pages, page_table, kbar, pos, max_pos, top
 # ----------------------------------------------------------------------------------------------
 # Dense serving path: packed prompts, the paged cache, and new or drafted tokens over it
 
+# The current stream of a device as an integer, and the current device; torch.cuda.current_stream()
+# builds a Stream object for it, 3.4 us of a 7 us call, and torch.cuda.current_device() looks first
+# whether CUDA is up, which a CUDA tensor has answered.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+_this_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _switch(dev, stream):
     """Where a call on a device has to switch first, the context for it: to the given stream (whose
     pool then owns what the call allocates), or to the tensors' device.  None: nothing to switch."""
@@ -511,15 +519,9 @@ def _switch(dev, stream):
         if stream.device != dev:
             raise ValueError(f"stream on {stream.device}, tensors on {dev}")
         return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
+    if dev.index != _this_device():
         return torch.cuda.stream(torch.cuda.current_stream(dev))
     return None
-
-
-# The current stream of a device as an integer; torch.cuda.current_stream() builds a Stream object
-# for it, 3.4 us of a 7 us call.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                      lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _fit(t, name, shape, dtype, dev):
