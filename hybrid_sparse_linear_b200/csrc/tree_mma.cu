@@ -133,6 +133,24 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         const int n = tree::run_tiles(c), t0 = tree::first_tile(c), end = t0 + n;
         if (n == 0) continue;
         const int64_t row0 = ((int64_t)c.b * s.Hkv + c.g) * s.rows;
+        // Q's fragments, on their way while the pages are found, and the rows' draft masks.
+        uint64_t bits[2];
+        uint32_t qa[kSteps][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = g + 8 * h;
+            const bool real = r < s.rows;
+            bits[h] = real ? tree::draft_bits(masks, c.b, r % s.T, s.T) : 0ull;
+            const __nv_bfloat16* src = q + (row0 + r) * D + t * kPer;
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st) {
+                const uint2 u = real ? __ldg(reinterpret_cast<const uint2*>(
+                                           src + (st / (kPer / 4)) * 4 * kPer + (st % (kPer / 4)) * 4))
+                                     : make_uint2(0u, 0u);
+                qa[st][h] = u.x;
+                qa[st][2 + h] = u.y;
+            }
+        }
         // This warp takes the run's pages warp, warp + kWarps, ...; lane i knows the page of the next
         // 32 of them that is its own i-th.
         int ids = -1, ids_at = -32;
@@ -140,8 +158,9 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
             if (i >= ids_at + 32) {
                 ids_at = i;
                 const int tl = t0 + warp + L::kWarps * (i + lane);
-                ids = tl < end ? page_of(pages, c.b, tl) : -1;
-                if (tl < end && ids < 0) flag(ctx, kStatusBounds);
+                ids = page_of(pages, c.b, tl);
+                if (tl >= end) ids = -1;
+                else if (ids < 0) flag(ctx, kStatusBounds);
             }
             return __shfl_sync(0xffffffffu, ids, i - ids_at);
         };
@@ -165,53 +184,36 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         load(id, true);
         load(id, false);
 
-        // Q's fragments and the rows' draft masks.
-        uint64_t bits[2];
         float sl[2] = {sl2, sl2};  // per row: from S to log2 units
         uint4* qf = reinterpret_cast<uint4*>(sm + L::kOffQ) + lane;
-        {
-            uint32_t qa[kSteps][4];
+        if constexpr (kCodes) {  // to fp16, the largest value in [2^kUpQ, 2^(kUpQ + 1))
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = g + 8 * h;
-                const bool real = r < s.rows;
-                bits[h] = real ? tree::draft_bits(masks, c.b, r % s.T, s.T) : 0ull;
-                const __nv_bfloat16* src = q + (row0 + r) * D + t * kPer;
+                uint32_t m = 0u;
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st)
+                    m = __vmaxu2(m, __vmaxu2(qa[st][h] & 0x7fff7fffu, qa[st][2 + h] & 0x7fff7fffu));
+                m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                int ex = (int)(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent
+                if (ex == 255) ex = 127;                         // an infinity or a NaN stays what it is
+                ex = max(ex, kUpQ + 1) - kUpQ;
+                const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+                sl[h] = sl2 * __uint_as_float((uint32_t)ex << 23);
+                auto half2 = [&](uint32_t w) {
+                    const __half2 v = __floats2half2_rn(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
+                    return *reinterpret_cast<const uint32_t*>(&v);
+                };
 #pragma unroll
                 for (int st = 0; st < kSteps; ++st) {
-                    const uint2 u = real ? __ldg(reinterpret_cast<const uint2*>(
-                                               src + (st / (kPer / 4)) * 4 * kPer + (st % (kPer / 4)) * 4))
-                                         : make_uint2(0u, 0u);
-                    qa[st][h] = u.x;
-                    qa[st][2 + h] = u.y;
-                }
-                if constexpr (kCodes) {  // to fp16, the largest value in [2^kUpQ, 2^(kUpQ + 1))
-                    uint32_t m = 0u;
-#pragma unroll
-                    for (int st = 0; st < kSteps; ++st)
-                        m = __vmaxu2(m, __vmaxu2(qa[st][h] & 0x7fff7fffu, qa[st][2 + h] & 0x7fff7fffu));
-                    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                    m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                    int ex = (int)(max(m & 0xffffu, m >> 16) >> 7);  // biased exponent
-                    if (ex == 255) ex = 127;                         // an infinity or a NaN stays what it is
-                    ex = max(ex, kUpQ + 1) - kUpQ;
-                    const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-                    sl[h] = sl2 * __uint_as_float((uint32_t)ex << 23);
-                    auto half2 = [&](uint32_t w) {
-                        const __half2 v = __floats2half2_rn(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
-                        return *reinterpret_cast<const uint32_t*>(&v);
-                    };
-#pragma unroll
-                    for (int st = 0; st < kSteps; ++st) {
-                        qa[st][h] = half2(qa[st][h]);
-                        qa[st][2 + h] = half2(qa[st][2 + h]);
-                    }
+                    qa[st][h] = half2(qa[st][h]);
+                    qa[st][2 + h] = half2(qa[st][2 + h]);
                 }
             }
-#pragma unroll
-            for (int st = 0; st < kSteps; ++st)  // every warp has them all; one puts them down
-                if (st % L::kWarps == warp) qf[st * 32] = make_uint4(qa[st][0], qa[st][1], qa[st][2], qa[st][3]);
         }
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st)  // every warp has them all; one puts them down
+            if (st % L::kWarps == warp) qf[st * 32] = make_uint4(qa[st][0], qa[st][1], qa[st][2], qa[st][3]);
         if constexpr (!kCodes) {
             if (tid == 0) noted = 0;
             for (int e = tid; e < 2 * D; e += L::kThreads) notes[e] = 0ull;
