@@ -15,6 +15,8 @@
 // line: per 128 keys it took 3900 cycles of which the tensor core worked 2048 (1008 TFLOP/s at 32768
 // tokens; two threads per row in that form, which have to meet for the row's maximum, 814).
 //
+// This form takes 8.0 ms there (1100 TFLOP/s), and 270 to 307 us for 16 prompts of 0 to 4096 tokens.
+//
 // Only the last key tile(s) hold keys that some row must not see.  There S and PV stop at the last
 // 16-key step a row sees, rows mask by their own position, and, since a probability of zero still
 // turns an infinity or NaN of V into NaN, one warp first looks through the V rows that not every

@@ -6,7 +6,9 @@
 // memory and TMEM costs more than the work, so each warp takes whole pages on its own: K and V of a
 // page land in the warp's own buffers by TMA (the next page's K is requested as soon as S is formed,
 // its V after P V), the products are m16n8k16 tiles, and codes become bf16 fragments in registers.
-// Twelve warps (six for bf16 rows of 256 bytes) keep about 150 KB per SM on their way.
+// Twelve warps (six for bf16 rows of 256 bytes) keep about 150 KB per SM on their way.  Measured, 32 query
+// heads of 128 over 2: one token over four int8 caches of 790000 tokens together 85 to 90 us (4.8 TB/s; on the
+// 128-row tiles 225), over one bf16 cache of 1000 10.5 to 10.9 us.
 //
 // Fragments.  The contraction over d may take its elements in any order as long as Q and K agree: a
 // lane reads 16 bytes of a key's row and uses them for consecutive steps of four elements, and Q's
