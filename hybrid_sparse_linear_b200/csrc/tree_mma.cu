@@ -186,7 +186,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         load(id, true);
         load(id, false);
 
-        float sl[2] = {sl2, sl2};  // per row: from S to log2 units
+        [[maybe_unused]] float up[2];  // per row: takes Q's lift back
         uint4* qf = reinterpret_cast<uint4*>(sm + L::kOffQ) + lane;
         if constexpr (kCodes) {  // to fp16, the largest value in [2^kUpQ, 2^(kUpQ + 1))
 #pragma unroll
@@ -201,7 +201,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 if (ex == 255) ex = 127;                         // an infinity or a NaN stays what it is
                 ex = max(ex, kUpQ + 1) - kUpQ;
                 const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-                sl[h] = sl2 * __uint_as_float((uint32_t)ex << 23);
+                up[h] = __uint_as_float((uint32_t)ex << 23);
                 auto half2 = [&](uint32_t w) {
                     const __half2 v = __floats2half2_rn(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
                     return *reinterpret_cast<const uint32_t*>(&v);
@@ -272,13 +272,17 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
             }
             if constexpr (kCodes) {
+                // From S to log2 units, before anything is hidden.  The factors are joined first: S holds Q's lift,
+                // which the key's scale alone would take out of fp32's range where keys are large and queries
+                // small; and up may be as small as 2^-126, so it comes last, where it can round to zero only
+                // what a logit cannot show.
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float a = ksc[8 * j + key_of<L>(2 * t)], b = ksc[8 * j + key_of<L>(2 * t + 1)];
-                    sc[j][0] *= a;
-                    sc[j][1] *= b;
-                    sc[j][2] *= a;
-                    sc[j][3] *= b;
+                    const float a = ksc[8 * j + key_of<L>(2 * t)] * sl2, b = ksc[8 * j + key_of<L>(2 * t + 1)] * sl2;
+                    sc[j][0] *= a * up[0];
+                    sc[j][1] *= b * up[0];
+                    sc[j][2] *= a * up[1];
+                    sc[j][3] *= b * up[1];
                 }
             }
             __syncwarp();
@@ -342,7 +346,7 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     const float va = vlg[8 * j + key_of<L>(2 * t)], vb = vlg[8 * j + key_of<L>(2 * t + 1)];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float y0 = sc[j][2 * h] *= sl[h], y1 = sc[j][2 * h + 1] *= sl[h];
+                        const float y0 = sc[j][2 * h], y1 = sc[j][2 * h + 1];
                         mx[h] = max3n(mx[h], y0, y1);
                         mv[h] = max3n(mv[h], y0 + va, y1 + vb);
                     }
