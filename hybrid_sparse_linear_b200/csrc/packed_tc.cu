@@ -27,8 +27,12 @@
 // tile B (thread = row); warp 8 issues the TMA loads; warps 9 and 10 issue the MMAs of tiles A and B;
 // warp 11 finds the units, two ahead, and looks through V.  Completions: the issuer commits once per round,
 // after PV(k) and S(k + 2), so the commit of round k + 2 says that both are done; two more rounds
-// without an S close a unit.  The softmax hands K and V stages back as it sees the commits.  Every
-// wait is bounded; a timeout sets the status word and all roles wind down.
+// without an S close a unit.  Those two have no P, by which the softmax tells the issuer that it has seen
+// a round, so units of even and odd number have barriers of their own: a unit that begins cannot turn
+// those on which a late softmax warp still waits for the end of the one before, and the unit after it,
+// which uses them again, begins when every warp has left that one (one set for all units: a warp that is
+// late by the next unit's first S waits for good).  The softmax hands K and V stages back as it sees
+// the commits.  Every wait is bounded; a timeout sets the status word and all roles wind down.
 #include <climits>
 
 #include "kv_format.cuh"
@@ -68,7 +72,8 @@ template <int kSlots>
 struct Bars {
     uint64_t full[kSlots], empty[kSlots];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2][2], p_full[2][2];  // per tile, alternating over the rounds
+    uint64_t s_full[2][2][2];  // per unit parity and tile, alternating over the unit's rounds
+    uint64_t p_full[2][2];     // per tile, alternating over the rounds with P
     uint64_t v_landed[2][4];  // V tiles to look through, per unit parity (at most four a unit)
     uint64_t v_seen[2];       // per unit parity: warp 11 is through with the unit
     uint64_t unit_full[2], unit_empty[2];
@@ -123,7 +128,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             mbar_init(&bars.q_full[x], 1);
             mbar_init(&bars.q_empty[x], 1);
             for (int j = 0; j < 2; ++j) {
-                mbar_init(&bars.s_full[x][j], 1);
+                for (int i = 0; i < 2; ++i) mbar_init(&bars.s_full[i][x][j], 1);
                 mbar_init(&bars.p_full[x][j], 4);
             }
             mbar_init(&bars.unit_full[x], 1);
@@ -229,7 +234,9 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const uint64_t k_d0 = dhi | sdesc_sw128_lo(smem_u32(sm + L::kOffRing), 16);
             const uint64_t v_d0 = dhi | sdesc_sw128_lo(smem_u32(sm + L::kOffRing), L::kBox);
             constexpr uint32_t idPV = idesc_bf16_f32(128, D, false, true);
-            uint32_t rc = 0, kq = 0, sr = 0, pr = 0;  // entries, Q tiles, rounds, rounds with P, before the unit
+            // Entries, Q tiles, rounds (of units of this one's parity; sr_next: of the other), rounds with P,
+            // before the unit.
+            uint32_t rc = 0, kq = 0, sr = 0, sr_next = 0, pr = 0;
             bool ok = true;
             Unit u;
             for (int it = 0; ok && take_unit(it, u); ++it) {
@@ -249,7 +256,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                             mma_ss_elect(dS + j * 64, q_d + (((ks >> 2) * L::kQBox + (ks & 3) * 32) >> 4),
                                          k_d + (((ks >> 2) * L::kBox + (ks & 3) * 32) >> 4), id, ks > 0 ? 1u : 0u);
                     }
-                    mma_commit_elect(&bars.s_full[x][j]);
+                    mma_commit_elect(&bars.s_full[it & 1][x][j]);
                     return true;
                 };
                 if (nx > 0) {
@@ -275,7 +282,9 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     }
                     ok = issue_s(b + 2);
                 }
-                if (nx > 0) sr += nx + 2;
+                const uint32_t rounds = nx > 0 ? sr + nx + 2 : sr;
+                sr = sr_next;
+                sr_next = rounds;
                 // Key tiles that only the other tile has: seen in order and handed back.
                 for (int b = nx; ok && b < n; ++b) {
                     for (int j = 0; ok && j < 2; ++j) {
@@ -388,7 +397,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const uint32_t colO = tmem + lane_base + kColO + x * 128;
         const uint32_t colS = tmem + lane_base + kColS + x * 128;
         const bool lead = (tid & 127) == 0;  // hands stages and Q back for the tile
-        uint32_t rc = 0, sr = 0, pr = 0;  // as the issuer's
+        uint32_t rc = 0, sr = 0, sr_next = 0, pr = 0;  // as the issuer's
         bool ok = true;
         Unit u;
         for (int it = 0; ok && take_unit(it, u); ++it) {
@@ -398,7 +407,7 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const int i = u.first + x * tq + r % tq;  // this row's token
             const int full_tiles = (u.first + x * tq + 1) / kK;  // key tiles that every row sees whole
             RowState st;
-            auto round = [&](int b) { return wait_warp(&bars.s_full[x][(sr + b) & 1], ((sr + b) >> 1) & 1, ctx, abort); };
+            auto round = [&](int b) { return wait_warp(&bars.s_full[it & 1][x][(sr + b) & 1], ((sr + b) >> 1) & 1, ctx, abort); };
             auto give = [&](int e) { mbar_arrive(&bars.empty[slot_of(rc + e)]); };
             for (int b = 0; b < nx; ++b, ++pr) {
                 ok = round(b);
@@ -508,6 +517,9 @@ packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 }
                 tc_fence_before();
             }
+            const uint32_t rounds = sr;
+            sr = sr_next;
+            sr_next = rounds;
             rc += 2 * n;
             leave_unit(it);
         }

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 import serving_plain as sp
-from test_gpu_serving import BF16, F32, NAN, _close, _tag, _tree_inputs, _tree_ref, _tree_run, sala  # noqa: F401
+from test_gpu_serving import (BF16, F32, NAN, _close, _packed_inputs, _tag, _tree_inputs, _tree_ref,  # noqa: F401
+                              _tree_run, sala)
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,18 @@ def test_tree_decode_large_keys_and_small_queries(sala, H, Hkv, T, d, fmt):  # n
     out = _tree_run(sala, q, cache, ctx, tree)
     sala.check_status()
     _close(out, *_tree_ref(q, cache, ctx, tree), max(ctx) + T, _tag(BF16, "large keys"))
+
+
+@pytest.mark.parametrize("H,Hkv,d,top,n", [(4, 4, 64, 300, 300), (4, 4, 128, 300, 250), (4, 2, 64, 300, 300),
+                                           (6, 2, 64, 300, 250), (6, 2, 128, 700, 60), (8, 2, 64, 200, 400)])
+def test_packed_prefill_several_units_per_block(sala, H, Hkv, d, top, n):  # noqa: F811
+    # many short units after one another in every block, the second tile of rows longer, as long or without
+    # a row; groups of one, two, three and four query heads
+    g = torch.Generator().manual_seed(33)
+    lens = [int(x) for x in torch.randint(0, top, (n,), generator=g)]
+    q, k, v = _packed_inputs(H, Hkv, d, BF16, sum(lens), seed=34)
+    args = q.cuda(), k.cuda(), v.cuda(), sp.offsets(lens).cuda()
+    a, b = (sala.packed_prefill(*args) for _ in range(2))
+    sala.check_status()
+    assert torch.equal(a, b)
+    _close(a, *sp.packed64(q, k, v, lens), top, "bf16 units")
