@@ -272,17 +272,18 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
             }
             if constexpr (kCodes) {
-                // From S to log2 units, before anything is hidden.  The factors are joined first: S holds Q's lift,
-                // which the key's scale alone would take out of fp32's range where keys are large and queries
-                // small; and up may be as small as 2^-126, so it comes last, where it can round to zero only
-                // what a logit cannot show.
+                // From S to log2 units, before anything is hidden.  The factors are joined first, the key's scale
+                // with what takes Q's lift back: alone the scale would bring S, which holds the lift, out of
+                // fp32's range where keys are large and queries small, and the other could round to zero.
+                // Together they leave the range only where q . k does.
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float a = ksc[8 * j + key_of<L>(2 * t)] * sl2, b = ksc[8 * j + key_of<L>(2 * t + 1)] * sl2;
-                    sc[j][0] *= a * up[0];
-                    sc[j][1] *= b * up[0];
-                    sc[j][2] *= a * up[1];
-                    sc[j][3] *= b * up[1];
+                    const float a = ksc[8 * j + key_of<L>(2 * t)], b = ksc[8 * j + key_of<L>(2 * t + 1)];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        sc[j][2 * h] *= a * up[h] * sl2;
+                        sc[j][2 * h + 1] *= b * up[h] * sl2;
+                    }
                 }
             }
             __syncwarp();

@@ -29,6 +29,21 @@ def test_tree_decode_small_queries_and_tiny_scales(sala, H, Hkv, T, dtype, fmt, 
     _close(out, *_tree_ref(q, cache, ctx, tree, scale), max(ctx) + T, _tag(dtype, "tiny scale"))
 
 
+@pytest.mark.parametrize("scale", [1e10, 2e38])
+@pytest.mark.parametrize("dtype,fmt", FORMS)
+@pytest.mark.parametrize("H,Hkv,T", [(32, 2, 1), (8, 4, 8), (32, 2, 8)])
+def test_tree_decode_zero_queries_and_large_scales(sala, H, Hkv, T, dtype, fmt, scale):  # noqa: F811
+    ctx = [70, 190, 0]
+    q, cache, tree = _tree_inputs(H, Hkv, 128, dtype, fmt, T, ctx, seed=31, fill=NAN)
+    q[:] = 0
+    # keys as large as the logits' factor allows (more rows than 16) or as large as they come
+    if cache.ks is not None and H // Hkv * T <= 16:
+        cache.ks *= 2.0 ** 120
+    out = _tree_run(sala, q, cache, ctx, tree, scale=scale)
+    sala.check_status()
+    _close(out, *_tree_ref(q, cache, ctx, tree, scale), max(ctx) + T, _tag(dtype, "large scale"))
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("H,Hkv,T", [(32, 2, 1), (8, 4, 8), (32, 2, 8)])
 @pytest.mark.parametrize("d", [64, 128])
