@@ -876,7 +876,9 @@ static sala_status check_dense(int B, int Hkv, int d, sala_dtype dt) {
 
 static sala_status check_heads(int H, int Hkv, float scale) {
     REQUIRE(H >= 0 && H % Hkv == 0, SALA_ERR_INVALID_ARG, "H %d must be a multiple of Hkv %d", H, Hkv);
-    REQUIRE(isfinite(scale) && scale >= 0.f, SALA_ERR_INVALID_ARG, "scale must be finite and >= 0");
+    // The kernels work in log2 units: the factor has to be a number there too.
+    REQUIRE(scale >= 0.f && isfinite(scale * 1.4426950408889634f), SALA_ERR_INVALID_ARG,
+            "scale must be >= 0 and finite, also times log2(e)");
     return SALA_OK;
 }
 

@@ -503,7 +503,7 @@ sala_status sala_sparse_decode_noalloc(const void* q, const void* kcache, const 
 /* Causal softmax attention over packed prompts:
  *   o_i = sum_{j} softmax_j(scale q_i . k_j) v_j  over the keys j <= i of row i's sequence.
  * q, o : [H, total, d] device, dt.   k, v : [Hkv, total, d] device, dt.   H a multiple of Hkv.
- * d    : 64 or 128.  scale: 0 selects 1/sqrt(d); finite and >= 0.
+ * d    : 64 or 128.  scale: 0 selects 1/sqrt(d); >= 0 and finite, also times log2(e).
  * A row's result depends on the rows it attends to alone: an infinity or a NaN in a later token or
  * in another sequence does not reach it. */
 sala_status sala_packed_prefill(const void* q, const void* k, const void* v,
@@ -549,7 +549,8 @@ sala_status sala_kv_read(const void* k_pages, const void* v_pages, const float* 
  * ctx        : [B] int32 device, each in [0, max_ctx] (outside: flagged and clamped).
  * max_ctx    : the largest context, max_ctx + T <= max_pages * 64, at most 2^30.
  * tree       : [B, T] uint64 device; bits at and above T are ignored.
- * scale      : 0 selects 1/sqrt(d); finite and >= 0.   d : 64 or 128.   block : 64.
+ * scale      : 0 selects 1/sqrt(d); >= 0 and finite, also times log2(e).   d : 64 or 128.
+ * block      : 64.
  * workspace  : at least sala_tree_decode_paged_workspace(...) bytes of device scratch, 16-byte
  *              aligned, no initial value needed, not shared with a concurrent call.
  * The sums over the keys are split over the SMs and joined in a fixed order: equal inputs give
