@@ -54,6 +54,11 @@ __device__ __forceinline__ void find_places(int (&place)[kRows], int32_t (&stage
         __syncthreads();
     }
     bool bad = false;
+    if (blockIdx.y == 0) {  // offsets out of order or outside [0, total], which a row's search need not meet
+        const int32_t* o = fits ? staged : cu;
+        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < B; i += (int64_t)gridDim.x * kThreads)
+            bad = bad || o[i] > o[i + 1] || o[i] < 0 || o[i + 1] > total;
+    }
     if (threadIdx.x < kRows) {
         const int r = r0 + threadIdx.x;
         place[threadIdx.x] = r < total ? place_of(fits ? staged : cu, pos, p, B, Hkv, r, &bad) : -1;

@@ -273,3 +273,30 @@ def test_pages_written_here_are_read_by_the_sparse_decode(sala, dtype):  # noqa:
         for h in range(kv * H // Hkv, (kv + 1) * H // Hkv):
             ref = sp.attention64(q[0, h:h + 1], k[kv], v[kv], seen)
             _close(o[0, h:h + 1], *ref, 64 * len(blocks), _tag(dtype, "sparse decode over written pages"))
+
+
+@pytest.mark.parametrize("B", [4, 1500])  # offsets in shared memory, and too many for it
+@pytest.mark.parametrize("at,off", [(1, 60), (2, 3), (0, -5), (-1, 140), (-2, 140)])
+def test_cache_calls_flag_offsets_out_of_order(sala, B, at, off):  # noqa: F811
+    # a pair that descends, also where no row can tell; a first offset below 0, a last one behind total
+    Hkv, d, total = 2, 64, 100
+    k, v = (torch.randn((Hkv, total, d), generator=torch.Generator().manual_seed(51)).to(BF16).cuda() for _ in range(2))
+    cu = torch.full((B + 1,), total, dtype=torch.int32)
+    cu[:4] = torch.tensor([0, 20, 40, 70])
+    good = cu.cuda()
+    cu[at] = off
+    table = torch.arange(4 * B, dtype=torch.int32).reshape(B, 4).cuda()
+    pos = torch.zeros(B, dtype=torch.int32).cuda()
+    kp, vp = (torch.zeros((4 * B, Hkv, 64, d), dtype=BF16).cuda() for _ in range(2))
+    for c, bad in ((cu.cuda(), True), (good, False)):
+        for call in (lambda: sala.kv_write(k, v, c, pos, table, kp, vp),
+                     lambda: sala.kv_read(kp, vp, table, c, pos, total, BF16)):
+            call()
+            if bad:
+                with pytest.raises(sala.SalaError) as err:
+                    sala.check_status()
+                assert err.value.code == sala.ERR_BOUNDS
+            else:
+                sala.check_status()
+    rk, rv = sala.kv_read(kp, vp, table, good, pos, total, BF16)
+    assert torch.equal(rk, k) and torch.equal(rv, v)
