@@ -17,6 +17,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 64;          // packed rows per block
 constexpr int kStaged = 1024;      // offsets kept in shared memory (a longer batch searches global memory)
+constexpr unsigned kCheckers = 1024;  // blocks at most that look through the offsets
 
 // Row of the cache ((page * Hkv + head) * 64 + slot, without the head's part), or -1: not in any
 // sequence, or on a page the table does not hold (the latter sets *bad).
@@ -54,14 +55,16 @@ __device__ __forceinline__ void find_places(int (&place)[kRows], int32_t (&stage
         __syncthreads();
     }
     bool bad = false;
-    if (blockIdx.y == 0) {  // offsets out of order or outside [0, total], which a row's search need not meet
-        const int32_t* o = fits ? staged : cu;
-        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < B; i += (int64_t)gridDim.x * kThreads)
-            bad = bad || o[i] > o[i + 1] || o[i] < 0 || o[i + 1] > total;
-    }
     if (threadIdx.x < kRows) {
         const int r = r0 + threadIdx.x;
         place[threadIdx.x] = r < total ? place_of(fits ? staged : cu, pos, p, B, Hkv, r, &bad) : -1;
+    } else if (blockIdx.y == 0 && blockIdx.x < kCheckers) {
+        // The other threads meanwhile look for offsets out of order or outside [0, total], which a row's search
+        // need not meet.
+        const int32_t* o = fits ? staged : cu;
+        for (unsigned i = blockIdx.x * (kThreads - kRows) + threadIdx.x - kRows; i < (unsigned)B;
+             i += min(gridDim.x, kCheckers) * (kThreads - kRows))
+            bad = bad || o[i] > o[i + 1] || o[i] < 0 || o[i + 1] > total;
     }
     if (bad) flag(ctx, kStatusBounds);
     __syncthreads();
