@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import serving_plain as sp
-from test_gpu_serving import (BF16, F32, NAN, _close, _packed_inputs, _tag, _tree_inputs, _tree_ref,  # noqa: F401
+from test_gpu_serving import (BF16, F32, NAN, PACKED, TREE, _close, _packed_inputs, _tag, _tree_inputs, _tree_ref,  # noqa: F401
                               _tree_run, sala)
 
 pytestmark = pytest.mark.gpu
@@ -300,3 +300,33 @@ def test_cache_calls_flag_offsets_out_of_order(sala, B, at, off):  # noqa: F811
                 sala.check_status()
     rk, rv = sala.kv_read(kp, vp, table, good, pos, total, BF16)
     assert torch.equal(rk, k) and torch.equal(rv, v)
+
+
+# ---------------------------------------------------------------------------------------------
+# The main cases of the bf16 kernels at the bound of the instructions that they use
+
+def _instruction_bound(A, e, n):
+    """serving_plain.bound for bf16 with its 1e-4 for the exponential replaced by what the kernels' own steps
+    cost: ex2.approx 2^-22 of a weight, lg2.approx (V's scales in exponents) 2^-22 of an exponent, both once more
+    in the normaliser, together at most 2^-20; and n + 8 additions in 32 bits, 2^-24 each."""
+    return A * (2 * e[..., None] + 2.0 ** -7 + 2.0 ** -20 + (n + 8) * 2.0 ** -24) + 1e-30
+
+
+@pytest.mark.parametrize("H,Hkv,d,dtype,lens", [c for c in PACKED if c[3] == BF16])
+def test_packed_cases_at_the_instructions_bound(sala, H, Hkv, d, dtype, lens):  # noqa: F811
+    q, k, v = _packed_inputs(H, Hkv, d, dtype, sum(lens), seed=61)
+    out = sala.packed_prefill(q.cuda(), k.cuda(), v.cuda(), sp.offsets(lens).cuda())
+    sala.check_status()
+    o, A, e = sp.packed64(q, k, v, lens)
+    assert bool(((out.double().cpu() - o).abs() <= _instruction_bound(A, e, max(lens))).all())
+
+
+@pytest.mark.parametrize("H,Hkv,d,dtype,fmt,T,ctx", [c for c in TREE if c[3] == BF16])
+def test_tree_cases_at_the_instructions_bound(sala, H, Hkv, d, dtype, fmt, T, ctx):  # noqa: F811
+    q, cache, tree = _tree_inputs(H, Hkv, d, dtype, fmt, T, ctx, seed=62, fill=NAN)
+    out = _tree_run(sala, q, cache, ctx, tree)
+    sala.check_status()
+    o, A, e = _tree_ref(q, cache, ctx, tree)
+    n = max(ctx) + T
+    floor = _floor(fmt, [cache.dense64(b, 0, c + T) for b, c in enumerate(ctx)], n) if H // Hkv * T <= 16 else 0.0
+    assert bool(((out.double().cpu() - o).abs() <= _instruction_bound(A, e, n) + floor).all())
