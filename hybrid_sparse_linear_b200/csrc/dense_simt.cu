@@ -29,7 +29,9 @@ namespace {
 constexpr int kKeys = 64;   // keys per tile: one page of the paged cache
 constexpr int kThreads = 256;
 constexpr int kPad = 4;     // floats: 16-byte rows that start 4 banks apart
-constexpr int kPad0 = 1;    // beginning an item costs about a tile
+// Beginning an item costs about a tile: one token of 16 heads per KV head over 16 int8 contexts of up to 9000 tokens
+// 82 us (0: 85, 3: 82).
+constexpr int kPad0 = 1;
 constexpr float kHidden = -1.f;  // P of a position its row does not see (probabilities are >= 0)
 
 // R: query rows per thread; a block has 16 R.

@@ -5,8 +5,8 @@
 // The maximum is kept stale until a row's new one exceeds it by more than 8 in log2 units: a
 // probability then stays below 2^8, which cancels in O / l, and the accumulator is rescaled only
 // in the rare step that passes the threshold.  All exponentials go to the multi-function unit: it is
-// busy 58 % of the time, and the issue slots are what runs short, of which a pair of FMA-pipe
-// exponentials (fastexp.cuh) takes about ten (one pair in four there: 4 % slower at 32768 tokens).
+// busy 54 % of the time (packed prompts, 12288 tokens), and a pair of FMA-pipe exponentials (fastexp.cuh) takes
+// about ten issue slots of the same warps (one pair in four there: 4 % slower at 32768 tokens).
 //
 // A NaN or +infinity among a row's visible logits makes its sum NaN (the maximum passes NaN on); a
 // hidden position is left out by selection.

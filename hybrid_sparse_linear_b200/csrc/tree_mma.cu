@@ -5,10 +5,12 @@
 // 8 bits.  A 128-row tensor-core tile would be seven eighths empty, and its chain through shared
 // memory and TMEM costs more than the work, so each warp takes whole pages on its own: K and V of a
 // page land in the warp's own buffers by TMA (the next page's K is requested as soon as S is formed,
-// its V after P V), the products are m16n8k16 tiles, and codes become bf16 fragments in registers.
-// Twelve warps (six for bf16 rows of 256 bytes) keep about 150 KB per SM on their way.  Measured, 32 query
-// heads of 128 over 2: one token over four int8 caches of 790000 tokens together 85 to 90 us (4.8 TB/s; on the
-// 128-row tiles 225), over one bf16 cache of 1000 10.5 to 10.9 us.
+// its V after P V), the products are m16n8k16 tiles, and codes become fp16 fragments in registers.
+// A page's K and V take 8, 16 or 32 KB (rows of 64, 128 or 256 bytes); twelve warps, six at 32 KB, keep up to
+// 96, 192 and 192 KB per SM on their way.  Measured, 32 query heads of 128 over 2: one token over four int8
+// caches of 790000 tokens together 85 to 90 us (4.8 TB/s; on the 128-row tiles 225), over one bf16 cache of
+// 1000 10.5 to 11.1 us.  At 168 registers the instances for rows of 128 codes spill, 24 bytes for int8, 148
+// for e4m3.
 //
 // Fragments.  The contraction over d may take its elements in any order as long as Q and K agree: a
 // lane reads 16 bytes of a key's row and uses them for consecutive steps of four elements, and Q's
@@ -23,8 +25,10 @@
 // smallest step then is 2^-39 of that value.  P has no such bound, as it carries the scales of V's
 // rows: the weight of key j in O is 2^(y_j + log2 sv_j - M + 7) with a running maximum M of its own
 // exponent, which is stale by at most 8, so that weights stay below 2^15 and vanish 2^-32 under the
-// largest of the warp's keys (a million of those lose 2^-12 of it); the weight in the row's sum is
-// 2^(y_j - m) as ever, and O is brought to m at the item's end.
+// largest of the warp's keys; the weight in the row's sum is 2^(y_j - m) as ever, and O is brought to m at
+// the item's end.  The accumulators hold 32 bits: in a column where the largest key's value is not small, what
+// one product of 16 keys adds is lost from 2^-24 of the sum down, long before fp16's steps count; those
+// show in columns where that value is 0 or nearly so.
 //
 // Hidden positions, infinities and NaN: as in the tensor-core kernel (tree_tc.cu).  The warps'
 // accumulators are joined in shared memory at an item's end.
@@ -559,7 +563,9 @@ tree_mma_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 // against 66), and is even at 128.
 int item_pages(int items, int sms) { return 4 * items >= 3 * sms ? 64 : 8 * items >= sms ? 24 : 16; }
 // Beginning an item (a round of loads that nothing overlaps, the warps' join) costs about as much as
-// this many pages.
+// this many pages, or some more.  In us, one token of 32 heads of 128 over 2: 40 int8 contexts of up to 16000
+// tokens 52 (4 pages: 60, 24: 50), 200 of up to 8000 109 (119, 105), 16 bf16 contexts of up to 9000 19.1
+// (22.0, 19.1).
 constexpr int kPad = 12;
 
 template <int D, KvFormat F>

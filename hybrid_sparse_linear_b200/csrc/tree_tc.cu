@@ -10,8 +10,10 @@
 //
 // Bound: HBM for few rows (a key and value row are read once per 256 query rows: 4 G T d flops
 // against 4 d bytes, 2 (d + 4) in 8 bits), the tensor pipe from about T = 16 at G = 16.  Measured, 32 query
-// heads of 128 over 2: 64 drafts over 131072 tokens, bf16, 140 us (980 TFLOP/s); 8 drafts over 16 e4m3 caches
-// of 94000 tokens together 45 us, where converting and softmax warps fill the issue slots (in the wide form 50).
+// heads of 128 over 2: 64 drafts over 131072 tokens, bf16, 140 us (980 TFLOP/s; 163 in a run of a second under
+// the power cap, at 1.7 GHz); 8 drafts over 16 e4m3 caches of 94000 tokens together 45 us (in the wide form 50),
+// where no unit is full -- issue slots 46 %, ALU 37 %, tensor pipe 14 % -- and a tile waits for the chain codes,
+// bf16 tile, S, softmax, PV.  The 8-bit instances start with 96 registers and spill 80 to 88 bytes.
 //
 // 8-bit caches.  Codes are at most 8 bits wide, so each is a bf16 number exactly; eight warps turn
 // the raw bytes of a tile into bf16 tiles in shared memory and the matrix products run as for bf16.
@@ -52,7 +54,10 @@ constexpr int kConvThreads = 256;
 inline int item_tiles(bool wide, long long items, int sms) {
     return 8 * items < 3 * sms ? 8 : (4 * items < 3 * sms ? 16 : 32) << (wide ? 1 : 0);
 }
-constexpr int kPad = 4;  // beginning an item (Q, the first tiles' chain, the epilogue) costs about four tiles
+// Beginning an item (Q, the first tiles' chain, the epilogue) costs at least four tiles.  In us, 16 contexts of up
+// to 9000 tokens: 8 drafts, e4m3 34 (1 tile: 46, 8: 33.5); 64 drafts, bf16 128 (195, 102); 32 drafts, int8 75.5 (88,
+// 75); 4 drafts over 40 bf16 contexts of up to 16000 80 (83, 75).
+constexpr int kPad = 4;
 
 template <int D, KvFormat F, bool kWide>
 struct Layout {

@@ -491,7 +491,8 @@ sala_status sala_sparse_decode_noalloc(const void* q, const void* kcache, const 
  * in rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of every head (cu_seqlens: [B + 1] int32 device,
  * ascending from 0, at most total; equal neighbours are an empty sequence).  Rows behind the last
  * sequence are neither read into any result nor written.  Offsets out of order are flagged
- * (SALA_ERR_BOUNDS through sala_check_status) and the rows they leave unclear are skipped.
+ * (SALA_ERR_BOUNDS through sala_check_status); rows that two sequences then claim are computed for
+ * either or left as they were, and rows of none are skipped.
  *
  * Pages hold 64 tokens of one sequence for every KV head: k_pages, v_pages [n_pages, Hkv, 64, d],
  * in the 8-bit formats with k_scale, v_scale [n_pages, Hkv, 64] fp32 (NULL otherwise).
@@ -504,6 +505,9 @@ sala_status sala_sparse_decode_noalloc(const void* q, const void* kcache, const 
  *   o_i = sum_{j} softmax_j(scale q_i . k_j) v_j  over the keys j <= i of row i's sequence.
  * q, o : [H, total, d] device, dt.   k, v : [Hkv, total, d] device, dt.   H a multiple of Hkv.
  * d    : 64 or 128.  scale: 0 selects 1/sqrt(d); >= 0 and finite, also times log2(e).
+ * H at most 65535.
+ * bf16: products are summed and softmax statistics held in 32 bits; each weight is rounded to bf16 before
+ * its product with v, and the output once.  fp32: every step in 32 bits on the CUDA cores.
  * A row's result depends on the rows it attends to alone: an infinity or a NaN in a later token or
  * in another sequence does not reach it. */
 sala_status sala_packed_prefill(const void* q, const void* k, const void* v,
@@ -547,12 +551,25 @@ sala_status sala_kv_read(const void* k_pages, const void* v_pages, const float* 
  * logits are all -infinity, gives 0.
  * q, o       : [B, H, T, d] device, dt.   1 <= T <= 64.
  * ctx        : [B] int32 device, each in [0, max_ctx] (outside: flagged and clamped).
- * max_ctx    : the largest context, max_ctx + T <= max_pages * 64, at most 2^30.
+ * max_ctx    : the largest context, max_ctx + T <= max_pages * 64, at most 2^30.  It also decides how the
+ *              work is split, so a bound far above the contexts costs time (one token over 1000 tokens, bf16:
+ *              10.9 us, in the split for long contexts 14.1): in a captured graph, whose max_ctx
+ *              stays, capture one graph per range of lengths.
  * tree       : [B, T] uint64 device; bits at and above T are ignored.
  * scale      : 0 selects 1/sqrt(d); >= 0 and finite, also times log2(e).   d : 64 or 128.
  * block      : 64.
  * workspace  : at least sala_tree_decode_paged_workspace(...) bytes of device scratch, 16-byte
  *              aligned, no initial value needed, not shared with a concurrent call.
+ * B * Hkv at most 65535, H / Hkv * T at most 2^20.
+ * bf16 queries: sums and softmax statistics are held in 32 bits and the output is rounded once.  Before its
+ * product with V a weight is rounded to bf16, over an 8-bit cache after it was multiplied by the scale of its
+ * row of V.  With at most 16 rows (H / Hkv * T) over an 8-bit cache that product is rounded to fp16 instead,
+ * whose smallest step is then at most 2^-31 of the largest product among the keys that one warp takes, and so
+ * are a row's queries, whose smallest step is at most 2^-38 of the row's largest; what is below half a smallest
+ * step counts as zero.  With more rows logits over an 8-bit cache are formed as (q . codes) (key scale * scale
+ * * log2 e) in 32 bits, and both factors have to stay finite there (|q| up to 2^112, a key's largest magnitude
+ * times scale up to 2^134).
+ * fp32 queries: every step in 32 bits on the CUDA cores.
  * The sums over the keys are split over the SMs and joined in a fixed order: equal inputs give
  * equal bits.  An infinity or a NaN in a new token reaches the rows that attend to it alone. */
 sala_status sala_tree_decode_paged(const void* q, const void* k_pages, const void* v_pages,
