@@ -499,6 +499,8 @@ sala_status sala_sparse_decode_noalloc(const void* q, const void* kcache, const 
  * page_table [B, max_pages] int32 device: entry [b][j] is the page of the tokens 64 j .. 64 j + 63
  * of sequence b.  An entry outside [0, n_pages) where one is needed is flagged (SALA_ERR_BOUNDS)
  * and what it should hold is left out.  Slots behind a sequence's last token may hold anything.
+ * sala_sparse_decode_paged reads the same pages in SALA_KV_SAME; rows held in 8 bits reach the sparse
+ * layers through sala_kv_read.
  */
 
 /* Causal softmax attention over packed prompts:
