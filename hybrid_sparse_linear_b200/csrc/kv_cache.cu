@@ -17,7 +17,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 64;          // packed rows per block
 constexpr int kStaged = 1024;      // offsets kept in shared memory (a longer batch searches global memory)
-constexpr unsigned kCheckers = 1024;  // blocks at most that look through the offsets
+constexpr unsigned kOffsetBlocks = 1024;  // blocks at most that look through the offsets
 
 // Row of the cache ((page * Hkv + head) * 64 + slot, without the head's part), or -1: not in any
 // sequence, or on a page the table does not hold (the latter sets *bad).
@@ -58,12 +58,12 @@ __device__ __forceinline__ void find_places(int (&place)[kRows], int32_t (&stage
     if (threadIdx.x < kRows) {
         const int r = r0 + threadIdx.x;
         place[threadIdx.x] = r < total ? place_of(fits ? staged : cu, pos, p, B, Hkv, r, &bad) : -1;
-    } else if (blockIdx.y == 0 && blockIdx.x < kCheckers) {
+    } else if (blockIdx.y == 0 && blockIdx.x < kOffsetBlocks) {
         // The other threads meanwhile look for offsets out of order or outside [0, total], which a row's search
         // need not meet.
         const int32_t* o = fits ? staged : cu;
         for (unsigned i = blockIdx.x * (kThreads - kRows) + threadIdx.x - kRows; i < (unsigned)B;
-             i += min(gridDim.x, kCheckers) * (kThreads - kRows))
+             i += min(gridDim.x, kOffsetBlocks) * (kThreads - kRows))
             bad = bad || o[i] > o[i + 1] || o[i] < 0 || o[i + 1] > total;
     }
     if (bad) flag(ctx, kStatusBounds);

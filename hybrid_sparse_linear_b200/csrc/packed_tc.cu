@@ -31,7 +31,7 @@
 // a round, so units of even and odd number have barriers of their own: a unit that begins cannot turn
 // those on which a late softmax warp still waits for the end of the one before, and the unit after it,
 // which uses them again, begins when every warp has left that one (one set for all units: a warp that is
-// late by the next unit's first S waits for good).  The softmax hands K and V stages back as it sees
+// late by the next unit's first S waits into the time limit).  The softmax hands K and V stages back as it sees
 // the commits.  Every wait is bounded; a timeout sets the status word and all roles wind down.
 #include <climits>
 
